@@ -1,0 +1,150 @@
+/*
+ * mapl_stage.h -- C ABI of the pipeline-stage operators that stand on both
+ * sides of a compressed boundary (mapl.h): the edge of a transformer block
+ * (dropout, norms, gate, residual) that forms the boundary activation X and
+ * feeds the first block behind it, and the blocks' projections in 8-bit
+ * floating point.  Same library, same conventions as mapl.h: contiguous
+ * row-major device pointers owned by the caller, no allocation, work enqueued
+ * on `stream` without synchronising, host validation before anything is
+ * enqueued, status codes MAPL_OK / MAPL_ERR_*.  Pointers need the alignment of
+ * their element type only, except packs and workspaces (16 bytes).
+ * `dt` (MAPL_BF16 or MAPL_F32) is the storage type of every floating-point
+ * tensor unless stated otherwise; arithmetic and sums are fp32, each output is
+ * rounded once to its type, nearest even.  Calls with no rows enqueue nothing
+ * except where an output has a value all the same (a zero gradient).
+ */
+#ifndef MAPL_STAGE_H
+#define MAPL_STAGE_H
+
+#include "mapl.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------------
+ * Dropout from a counter-based generator.  No mask is stored: whether element
+ * (n, c) is kept is a function of (seed, offset + n, c), so the backward pass
+ * is the same call on the gradient, and a recomputed or resharded micro-batch
+ * sees the same mask.
+ *
+ *   t    = floor(65536 p + 1/2)
+ *   keep = u16(n, c) >= t
+ *   Y    = keep ? X * 65536 / (65536 - t) : 0
+ *
+ * u16(n, c) is 16 bits of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel
+ * Random Numbers: As Easy as 1, 2, 3", SC 2011): counter words (c / 8,
+ * lo32(offset + n), hi32(offset + n), 0), key words (lo32(seed), hi32(seed));
+ * column c takes the (c mod 8)-th 16-bit field of the 128 output bits, lowest
+ * first.  p is thereby rounded to a multiple of 2^-16, and the scale is that of
+ * the rounded probability, so the expectation is exact.  A program advances
+ * `offset` by N from call to call.  A dropped place is 0 whatever X holds there
+ * (infinities and NaN too); p = 0 copies X, and a p that rounds to 1 gives zeros.
+ * X and Y may be the same tensor.  0 <= p <= 1 (MAPL_ERR_ARG); 0 <= N <=
+ * 2^31 - 1, 1 <= d <= 2^31 - 8, N d <= 2^36 (MAPL_ERR_SHAPE).
+ * ---------------------------------------------------------------------- */
+int stage_dropout(const void* X, void* Y, double p, uint64_t seed, uint64_t offset, int64_t N, int64_t d,
+                  mapl_dtype dt, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The edge of a block, one pass: with Y the block's output and X the residual
+ * stream, row by row
+ *
+ *   u     = dropout(Y)                                   (p, seed, offset as above)
+ *   v     = w_post * u / sqrt(mean(u^2) + eps)           (w_post NULL: v = u)
+ *   X_out = res_scale * X + gate[g] * v                  (gate NULL: 1)
+ *   H     = w_pre * X_out / sqrt(mean(X_out^2) + eps)    (H NULL: not formed)
+ *
+ * X_out is what mapl_compress takes at the end of a stage; H is what the next
+ * block's projections take.  H is formed from X_out before its rounding.
+ * w_post, w_pre [d].  gate [gate_rows][d]: gate_rows divides N, and row n
+ * reads gate row n / (N / gate_rows): 1 row is a gate per channel, B rows one
+ * per sequence, N rows one per token (gate NULL: gate_rows must be 0).
+ * Y NULL is the norm in front of the first block behind a boundary:
+ * X_out = res_scale * X (w_post, gate NULL and p = 0 then).  X_out NULL is not
+ * stored; X_out and H may not both be NULL; w_pre is given exactly with H.
+ * Outputs may not alias inputs, except that X_out may be X or Y.
+ * eps > 0, finite; res_scale finite (MAPL_ERR_ARG); 1 <= d <= 8192,
+ * 0 <= N <= 2^31 - 1 (MAPL_ERR_SHAPE).
+ * ---------------------------------------------------------------------- */
+int stage_norm(const void* X, const void* Y, const void* w_post, const void* gate, const void* w_pre, void* X_out,
+               void* H, float res_scale, float eps, double p, uint64_t seed, uint64_t offset, int64_t N, int64_t d,
+               int64_t gate_rows, mapl_dtype dt, hipStream_t stream);
+
+/* Backward of stage_norm.  Given gX_out = dL/dX_out and gH = dL/dH (either may
+ * be NULL for zero, not both), with a = gH * w_pre, r = 1/sqrt(mean(X_out^2) +
+ * eps), q = 1/sqrt(mean(u^2) + eps) (q = 1 and no mean term without w_post):
+ *
+ *   t        = gX_out + r (a - X_out r^2 mean(a X_out))
+ *   gX       = res_scale * t
+ *   b        = t * gate * w_post
+ *   gY       = dropout(q (b - u q^2 mean(b u)))
+ *   g_w_pre  = sum_n gH r X_out,   g_w_post = sum_n t gate q u
+ *   g_gate   = sum over the rows n of each gate row of t w_post q u
+ *
+ * It takes the stored X_out (only with gH) and Y, no statistics: both norms'
+ * sums are formed again from the row it reads anyway.  g_w_post, g_w_pre [d]
+ * and g_gate [gate_rows][d] are fp32; accumulate = 1 adds into them.  Each is
+ * required exactly when its weight (w_post, gate; w_pre with gH) is given; gX
+ * always, gY exactly when Y is.  With N = 0 each gradient given is zeroed.  The sums over rows have a fixed split and
+ * order (no floating-point atomics): results are bitwise repeatable.  `ws` of
+ * stage_norm_bwd_workspace_bytes() holds the partial sums, 16-byte aligned
+ * (MAPL_ERR_ARG); it may be NULL when that is 0.  gX may be gX_out and gY may
+ * be gH or Y.  Other rules as for stage_norm. */
+size_t stage_norm_bwd_workspace_bytes(int64_t N, int64_t d, int64_t gate_rows);
+int stage_norm_bwd(const void* gX_out, const void* gH, const void* X_out, const void* Y, const void* w_post,
+                   const void* gate, const void* w_pre, void* gX, void* gY, float* g_w_post, float* g_gate,
+                   float* g_w_pre, int accumulate, float res_scale, float eps, double p, uint64_t seed,
+                   uint64_t offset, int64_t N, int64_t d, int64_t gate_rows, mapl_dtype dt, void* ws,
+                   size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point (OCP e4m3) with one scale for each block of 128.
+ *
+ * A pack holds a matrix Q [rows][cols] as operand of fp8_gemm, contracted over
+ * its columns: e4m3 codes and, for each row and each 128 columns, a power of
+ * two 2^s kept as its biased exponent (one byte).  The block's scale is the
+ * smallest 2^s >= 2^-126 with max |x| <= 448 * 2^s (over finite elements), and
+ * an element stands for e4m3(x 2^-s) 2^s, nearest even.  Powers of two lose
+ * nothing against other scales (the codes float), round nothing themselves and
+ * are applied by the matrix cores.  A non-finite element becomes NaN.
+ * `square` = 1 gives one scale to each 128 x 128 block (weights: W and its
+ * transpose then hold the same values); 0 gives one to each row's 128 columns
+ * (tokens).  cols is padded to a multiple of 128 with zeros.
+ *
+ * fp8_pack reads X [R][C] once and writes pk, the operand [R][C], and / or
+ * pkT, the operand [C][R] of its transpose (scaled per column and 128 rows of
+ * X): forward Y = X W^T takes (X, W), gX = gY W takes (gY, W^T) and gW = gY^T X
+ * takes (gY^T, X^T).  Either may be NULL, not both.  Packs are 16-byte aligned
+ * (MAPL_ERR_ARG) and at least fp8_pack_bytes() of their own rows and columns
+ * (MAPL_ERR_WORKSPACE).  0 <= R, C <= 2^30, R C <= 2^36
+ * (MAPL_ERR_SHAPE).
+ * ---------------------------------------------------------------------- */
+size_t fp8_pack_bytes(int64_t rows, int64_t cols);
+int fp8_pack(const void* X, void* pk, size_t pk_bytes, void* pkT, size_t pkT_bytes, int square, int64_t R,
+             int64_t C, mapl_dtype dt, hipStream_t stream);
+
+/* X [rows][cols]: the values that a pack stands for, rounded to dt. */
+int fp8_unpack(const void* pk, size_t pk_bytes, void* X, int64_t rows, int64_t cols, mapl_dtype dt,
+               hipStream_t stream);
+
+/* C [M][N] (+)= A B^T for packs A of [M][K] and B of [N][K], rounded once to
+ * `dt`.  An fp32 C has fp32 sums of exact products (operand values below 2^-126
+ * may count as zero).  A bf16 C comes from the e4m3 matrix instruction, twice as
+ * fast, which keeps 13 bits below the largest of a few neighbouring products
+ * before they enter its fp32 accumulator: about 1.5e-5 of the sum's size, far
+ * below the output's rounding (2^-8).  accumulate = 1 adds into an fp32 C
+ * (MAPL_ERR_ARG for bf16, which would round twice).  Few output tiles with a
+ * long K are split over K; the partial sums go to `ws` of
+ * fp8_gemm_workspace_bytes() (may be NULL when that is 0; 16-byte aligned) and
+ * are joined in a fixed order, so results are bitwise repeatable.  K = 0 gives
+ * zeros.  Sizes as for fp8_pack. */
+size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int fp8_gemm(const void* pkA, size_t pkA_bytes, const void* pkB, size_t pkB_bytes, void* C, int accumulate,
+             int64_t M, int64_t N, int64_t K, mapl_dtype dt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MAPL_STAGE_H */

@@ -10,7 +10,8 @@ and a missing library raises.
 The method is that of "Learned Subspace Compression for Communication-
 Efficient Pipeline Parallelism" (MAPL): Eq. (1)-(3) codec, its backward, the
 residual VQ of Section 3.5 with the streaming sync of Appendix F, and the SPEL
-projector update of Section 3.3.
+projector update of Section 3.3.  The operators of the stage on either side of the boundary (block
+edge, dropout, 8-bit products) are in ``stage`` and exported here as well.
 """
 from __future__ import annotations
 
@@ -28,6 +29,8 @@ __all__ = [
     "rvq_encode", "rvq_decode", "rvq_stream_apply", "rvq_stream_decode", "spel_workspace_bytes", "spel_step",
     "spel_step_static", "spel_step_polar_express", "spel_polar_express_coefficients",
     "MAPL_F32", "MAPL_BF16",
+    "stage_dropout", "stage_norm", "stage_norm_bwd_workspace_bytes", "stage_norm_bwd",
+    "fp8_pack_bytes", "fp8_pack", "fp8_unpack", "fp8_gemm_workspace_bytes", "fp8_gemm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -509,3 +512,10 @@ def spel_polar_express_coefficients(ell: float, steps: int):
     _check(load().spel_polar_express_coefficients(float(ell), int(steps), coef.ctypes.data, err.ctypes.data),
            "spel_polar_express_coefficients")
     return coef, err
+
+
+# pipeline-stage operators (include/mapl_stage.h)
+from .stage import (  # noqa: E402,F401
+    stage_dropout, stage_norm, stage_norm_bwd_workspace_bytes, stage_norm_bwd,
+    fp8_pack_bytes, fp8_pack, fp8_unpack, fp8_gemm_workspace_bytes, fp8_gemm,
+)

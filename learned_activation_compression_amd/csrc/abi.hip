@@ -75,22 +75,6 @@ namespace {
 constexpr const char* kVersion = "mapl-gfx950 0.1.0";
 constexpr int kMaxPolarSteps = 32;
 
-// Launch status: clears any error left by an earlier call and prepares the
-// current device (the dynamic-LDS limits) before anything is enqueued; an
-// entry point returns MAPL_ERR_HIP without launching when that fails
-// (ready() false), and reports the launch error (if any) afterwards.
-struct LaunchScope {
-  hipError_t prep;
-  LaunchScope() {
-    (void)hipGetLastError();
-    prep = lds_prepare_device();
-  }
-  bool ready() const { return prep == hipSuccess; }
-  int done() const { return hipGetLastError() == hipSuccess ? MAPL_OK : MAPL_ERR_HIP; }
-};
-
-inline bool dtype_ok(mapl_dtype dt) { return dt == MAPL_F32 || dt == MAPL_BF16; }
-
 // Shared shape rules of the codec entry points.  ra is the anchor rank
 // (0: no anchor); the id range V matters only when an anchor is read.
 int check_codec_shape(int64_t B, int64_t T, int64_t d, int64_t r, int64_t ra, int64_t V, mapl_dtype dt, bool needV) {

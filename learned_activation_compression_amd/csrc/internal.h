@@ -4,11 +4,31 @@
 
 #include <hip/hip_runtime.h>
 
+#include "../../include/mapl.h"
 #include "common.h"
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace mapl {
+
+// ---- shared by the ABI layers (abi.hip, stage_abi.hip)
+// Launch status: clears any error left by an earlier call and prepares the
+// current device (the dynamic-LDS limits) before anything is enqueued; an
+// entry point returns MAPL_ERR_HIP without launching when that fails
+// (ready() false), and reports the launch error (if any) afterwards.
+struct LaunchScope {
+  hipError_t prep;
+  LaunchScope() {
+    (void)hipGetLastError();
+    prep = lds_prepare_device();
+  }
+  bool ready() const { return prep == hipSuccess; }
+  int done() const { return hipGetLastError() == hipSuccess ? MAPL_OK : MAPL_ERR_HIP; }
+};
+
+inline bool dtype_ok(mapl_dtype dt) { return dt == MAPL_F32 || dt == MAPL_BF16; }
 
 // ---- packed weights (bf16, fragment order; see pack.hip):
 //   AtF = A^T (r x d), AF = A (d x r), PtF = P^T (d x r), QnF = -(P A)^T (r x r),
@@ -119,5 +139,36 @@ void launch_spel_pe(float* A, const float* g, float* m, float alpha, float beta,
                     hipStream_t s);
 void launch_spel(float* A, const float* g, float* m, float alpha, float beta, int ns_iters,
                  float* D_out, int* status, int d, int r, void* ws, hipStream_t s);
+
+// ---- pipeline-stage operators (include/mapl_stage.h)
+void launch_dropout(const void* X, void* Y, double p, uint64_t seed, uint64_t offset, int64_t N, int64_t d, int bf16,
+                    hipStream_t s);
+struct StageNorm {  // the forward call's arguments; the backward reads X_out and leaves X and H unset
+  const void *X, *Y, *w_post, *gate, *w_pre;
+  void *X_out, *H;
+  float res_scale, eps;
+  double p;
+  uint64_t seed, offset;
+  int64_t N, d, gate_rows;
+};
+struct StageNormGrads {
+  const void *gX_out, *gH;
+  void *gX, *gY;
+  float *g_w_post, *g_gate, *g_w_pre;
+  int accumulate;
+  float* ws;
+};
+void launch_stage_norm(const StageNorm& c, int bf16, hipStream_t s);
+size_t stage_norm_bwd_ws_bytes(int64_t N, int64_t d, int64_t gate_rows);
+void launch_stage_norm_bwd(const StageNorm& c, const StageNormGrads& g, int bf16, hipStream_t s);
+
+// 8-bit packs: codes in matrix-core fragment order, then the block exponents
+size_t fp8_bytes(int64_t rows, int64_t cols);
+void launch_fp8_pack(const void* X, uint8_t* pk, uint8_t* pkT, int square, int64_t R, int64_t C, int bf16,
+                     hipStream_t s);
+void launch_fp8_unpack(const uint8_t* pk, void* X, int64_t rows, int64_t cols, int bf16, hipStream_t s);
+size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
+void launch_fp8_gemm(const uint8_t* A, const uint8_t* B, void* C, int accumulate, int64_t M, int64_t N, int64_t K,
+                     int bf16, float* ws, hipStream_t s);
 
 }  // namespace mapl

@@ -16,9 +16,11 @@ Modules
          polar for the LMO direction and the retraction (algorithm steps).
   rvq    Section 3.5 residual multi-codebook VQ encode / decode and the
          streaming codebook sync of Appendix F (algorithm steps).
+  stage  the operators of the stage around the boundary: dropout, block edge,
+         8-bit rounding (plain definitions, pinned by tests/test_stage_host.py).
 
 Parity status: every function here is pinned by tests/test_oracle_pins.py
 (brute-force loops, closed forms via the SVD, invariants stated on the pages,
 library special cases and the paper's printed payload sizes).
 """
-from . import codec, spel, rvq  # noqa: F401
+from . import codec, spel, rvq, stage  # noqa: F401
