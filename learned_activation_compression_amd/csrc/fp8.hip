@@ -11,6 +11,8 @@
 //    slack, so that 256 bytes from any multiple of 128 rows can be read.
 // Codes of padding rows are zero or stale: they only reach output rows that are
 // not stored.  Padding columns are zero in every pack.
+#include <type_traits>
+
 #include "internal.h"
 
 namespace mapl {
@@ -231,11 +233,13 @@ __global__ __launch_bounds__(256) void k_fp8_unpack(View p, T* X, int64_t rows, 
 }
 
 // ---------------------------------------------------------------------- gemm --
-// Lane l copies 4 bytes from g to LDS byte address (l_base + 4 l); otherwise as
-// copy16_to_lds.
-__device__ __forceinline__ void copy4_to_lds(const void* g, const void* l_base) {
-  const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(l_base)));
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(g), "s"(la) : "memory", "m0");
+// Lane l copies 16 (4) bytes from base + 16 l (base + 4 l), base uniform over the
+// wave, to LDS byte address lds + 16 l (lds + 4 l); otherwise as copy16_to_lds.
+__device__ __forceinline__ void copy_lane16_to_lds(const uint8_t* base, uint32_t lane_off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(lane_off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void copy_lane4_to_lds(const uint8_t* base, uint32_t lane_off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(lane_off), "s"(base), "s"(lds) : "memory", "m0");
 }
 
 __device__ __forceinline__ f32x16 mfma_e4m3(i32x8 a, i32x8 b, f32x16 c, int ea, int eb) {
@@ -263,13 +267,15 @@ struct GemmArgs {
   void* C;
   int64_t M, N;
   int accumulate;
+  int splits;      // parts of the contraction; more than one: partial sums [splits][M][N] fp32 in C
+  int64_t kb_per;  // blocks of 128 in each part
 };
 
-// Tile of WM * FM x WN * FN units of 32: WM x WN waves of FM x FN MFMA tiles.
+// Tile of (WM FM) x (WN FN) units of 32: WM x WN waves of FM x FN MFMA tiles.
 // B (columns of C) is the matrix cores' row operand and A their column operand,
 // so a lane's accumulators run along a row of C.
 //
-// Two ways to multiply, by the output's type:
+// Two ways to multiply, by the output's type (EXACT):
 //  - bf16: the scaled e4m3 matrix instruction, 2.0x the rate of the other.  It
 //    aligns the products of a few neighbouring columns to the largest of them and
 //    keeps 13 bits below it before they enter the fp32 accumulator: 1.5e-5 of the
@@ -283,36 +289,74 @@ struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kBM = WM * FM, kBN = WN * FN;  // units of 32 rows
   static constexpr int kUnits = kBM + kBN;
-  static constexpr int kStage = kUnits * 4096 + 512;  // codes, then 256 + 256 bytes of exponents
+  static constexpr int kStage = kUnits * 4096 + 512;   // codes, then 256 + 256 bytes of exponents
   static constexpr int kPieces = kUnits * 4 / kWaves;  // 1 KB pieces each wave copies per stage
   static constexpr int kLds = 2 * kStage;
-  static_assert(kUnits * 4 % kWaves == 0 && kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
+  static_assert(kUnits * 4 % kWaves == 0 && kPieces % 4 == 0 && kPieces % FM == 0 && (FM + FN) % FM == 0 && kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
 };
 
-template <typename T, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g) {
+// One row of a wave's output block from LDS to C: 16 bytes per lane.
+__device__ __forceinline__ void put16(bf16_t* c, const char* src, int64_t left, int) {
+  const u32x4 v = *reinterpret_cast<const u32x4*>(src);
+  if (left >= 8) {
+    *reinterpret_cast<u32x4_a2*>(c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) c[i] = static_cast<bf16_t>(v[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void put16(float* c, const char* src, int64_t left, int accumulate) {
+  f32x4 v = *reinterpret_cast<const f32x4*>(src);
+  typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+  if (left >= 4) {
+    if (accumulate) v += *reinterpret_cast<const f32x4_a4*>(c);
+    *reinterpret_cast<f32x4_a4*>(c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) c[i] = accumulate ? c[i] + v[i] : v[i];
+  }
+}
+
+// The loop runs one stage (128 columns) ahead in LDS and one step (64 columns)
+// ahead in registers, with one barrier a stage: behind it the stage just read is
+// free for the copy of the stage after next, and the next one is complete.
+template <typename T, bool EXACT, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
   using TL = Tile<WM, WN, FM, FN>;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int w = wave_id(), l = threadIdx.x & 63, wm = w / WN, wn = w % WN;
+  const uint32_t tiles_m = static_cast<uint32_t>((g.A.RT + TL::kBM - 1) / TL::kBM);
   const uint32_t tiles_n = static_cast<uint32_t>((g.B.RT + TL::kBN - 1) / TL::kBN);
-  const int64_t tm = int64_t(blockIdx.x / tiles_n) * TL::kBM, tn = int64_t(blockIdx.x % tiles_n) * TL::kBN;  // first unit row of each side
-  const int64_t KB = g.A.KB;
+  // the tiles of an XCD are neighbours: groups of 8 tile rows, column by column
+  uint32_t id = xcd_swizzle(blockIdx.x, gridDim.x);
+  const uint32_t split = id / (tiles_m * tiles_n);
+  id -= split * tiles_m * tiles_n;
+  const uint32_t grp = id / (8 * tiles_n), gh = min(8u, tiles_m - 8 * grp), in = id - grp * 8 * tiles_n;
+  const int64_t tm = int64_t(8 * grp + in % gh) * TL::kBM, tn = int64_t(in / gh) * TL::kBN;  // first unit rows
+  const int64_t KB = g.A.KB, k0 = split * g.kb_per, k1 = min(k0 + g.kb_per, KB);
 
-  // this wave's source pieces of a stage (unit rows past the end repeat the last one)
-  const uint8_t* src[TL::kPieces];
+  // this wave's units of a stage (unit rows past the end repeat the last one)
+  const uint8_t* src[TL::kPieces / 4];
 #pragma unroll
-  for (int i = 0; i < TL::kPieces; ++i) {
-    const int p = w * TL::kPieces + i, u = p >> 2;
-    const View& v = u < TL::kBM ? g.A : g.B;
-    const int64_t rt = min(u < TL::kBM ? tm + u : tn + (u - TL::kBM), v.RT - 1);
-    src[i] = v.code + rt * KB * 4096 + (p & 3) * 1024 + l * 16;
+  for (int i = 0; i < TL::kPieces / 4; ++i) {
+    const int u = w * (TL::kPieces / 4) + i;
+    const bool isA = u < TL::kBM;
+    const int64_t rt = isA ? min(tm + u, g.A.RT - 1) : min(tn + (u - TL::kBM), g.B.RT - 1);
+    src[i] = (isA ? g.A.code : g.B.code) + rt * KB * 4096;
   }
-  auto fetch = [&](int64_t kb) {
-    char* st = smem + (kb & 1) * TL::kStage;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(smem)));
+  const uint8_t* exps = (w & 1) ? g.B.exp + tn * 32 : g.A.exp + tm * 32;
+  const int64_t exp_stride = (w & 1) ? g.B.exp_stride : g.A.exp_stride;
+  // part i of FM of the copies of a stage
+  auto fetch = [&](int64_t kb, int i) {
+    const uint32_t st = lds0 + static_cast<uint32_t>(kb & 1) * TL::kStage;
 #pragma unroll
-    for (int i = 0; i < TL::kPieces; ++i) copy16_to_lds(src[i] + kb * 4096, st + (w * TL::kPieces + i) * 1024);
-    if (w == 0) copy4_to_lds(g.A.exp + kb * g.A.exp_stride + tm * 32 + l * 4, st + TL::kUnits * 4096);
-    if (w == 1) copy4_to_lds(g.B.exp + kb * g.B.exp_stride + tn * 32 + l * 4, st + TL::kUnits * 4096 + 256);
+    for (int p = i * (TL::kPieces / FM); p < (i + 1) * (TL::kPieces / FM); ++p)
+      copy_lane16_to_lds(src[p >> 2] + kb * 4096 + (p & 3) * 1024, l * 16, st + (w * TL::kPieces + p) * 1024);
+    // even waves copy A's exponents, odd ones B's: more often than needed, but without a branch
+    if (i == 0) copy_lane4_to_lds(exps + kb * exp_stride, l * 4, st + TL::kUnits * 4096 + (w & 1) * 256);
   };
 
   f32x16 acc[FM][FN];
@@ -323,79 +367,178 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
 
-  fetch(0);
-  for (int64_t kb = 0; kb < KB; ++kb) {
-    wait_vmcnt<0>();
-    __syncthreads();  // stage kb is in LDS, and every wave is done with the other one
-    if (kb + 1 < KB) fetch(kb + 1);
-    const char* st = smem + (kb & 1) * TL::kStage;
-    const char* ex = st + TL::kUnits * 4096;
+  struct Step {  // operands of 64 columns
+    i32x8 a[FM], b[FN];
     int ea[FM], eb[FN];
+  };
+  Step s0, s1;
+  // part i of FM of the operands of step s of stage kb; the column operand first, every row needs it
+  auto read = [&](Step& st, int64_t kb, int s, int i) {
+    const char* at = smem + (kb & 1) * TL::kStage + s * 2048 + l * 16;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) ea[i] = static_cast<uint8_t>(ex[(wm * FM + i) * 32 + (l & 31)]);
+    for (int f = i * (FM + FN) / FM; f < (i + 1) * (FM + FN) / FM; ++f) {
+      if (f < FN)
+        st.b[f] = ld_frag(at + (TL::kBM + wn * FN + f) * 4096);
+      else
+        st.a[f - FN] = ld_frag(at + (wm * FM + f - FN) * 4096);
+    }
+  };
+  auto read_exp = [&](Step& st, int64_t kb) {
+    const char* ex = smem + (kb & 1) * TL::kStage + TL::kUnits * 4096 + (l & 31);
 #pragma unroll
-    for (int i = 0; i < FN; ++i) eb[i] = static_cast<uint8_t>(ex[256 + (wn * FN + i) * 32 + (l & 31)]);
+    for (int i = 0; i < FM; ++i) st.ea[i] = static_cast<uint8_t>(ex[(wm * FM + i) * 32]);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      i32x8 a[FM], b[FN];
+    for (int i = 0; i < FN; ++i) st.eb[i] = static_cast<uint8_t>(ex[256 + (wn * FN + i) * 32]);
+  };
+  // row i of the wave's MFMA tiles
+  auto multiply = [&](const Step& st, int i) {
+    if constexpr (!EXACT) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) a[i] = ld_frag(st + (wm * FM + i) * 4096 + s * 2048 + l * 16);
+      for (int k = 0; k < FN; ++k) acc[i][k] = mfma_e4m3(st.b[k], st.a[i], acc[i][k], st.eb[k], st.ea[i]);
+    } else {
 #pragma unroll
-      for (int i = 0; i < FN; ++i) b[i] = ld_frag(st + (TL::kBM + wn * FN + i) * 4096 + s * 2048 + l * 16);
-      if constexpr (sizeof(T) == 2) {
+      for (int c = 0; c < 4; ++c) {
+        const bf16x8 wa = widen8(st.a[i][2 * c], st.a[i][2 * c + 1], __uint_as_float(uint32_t(st.ea[i]) << 23));
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int k = 0; k < FN; ++k) acc[i][k] = mfma_e4m3(b[k], a[i], acc[i][k], eb[k], ea[i]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          bf16x8 wa[FM], wb[FN];
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-            wa[i] = widen8(a[i][2 * c], a[i][2 * c + 1], __uint_as_float(uint32_t(ea[i]) << 23));
-#pragma unroll
-          for (int i = 0; i < FN; ++i)
-            wb[i] = widen8(b[i][2 * c], b[i][2 * c + 1], __uint_as_float(uint32_t(eb[i]) << 23));
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int k = 0; k < FN; ++k) acc[i][k] = mfma_bf16_32x32x16(wb[k], wa[i], acc[i][k]);
-        }
+        for (int k = 0; k < FN; ++k)
+          acc[i][k] = mfma_bf16_32x32x16(
+              widen8(st.b[k][2 * c], st.b[k][2 * c + 1], __uint_as_float(uint32_t(st.eb[k]) << 23)), wa, acc[i][k]);
       }
     }
-  }
+  };
 
-  // acc[i][k]: row (tm + wm FM + i) * 32 + (l & 31) of C, columns (tn + wn FN + k) * 32 + mfma32_row(v, l >> 5)
-  T* C = static_cast<T*>(g.C);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) fetch(k0, i);
+  wait_vmcnt<0>();
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int64_t m = (tm + wm * FM + i) * 32 + (l & 31);
-    if (m >= g.M) continue;
+    if (k0 + 1 < k1) fetch(k0 + 1, i);
+    read(s0, k0, 0, i);
+  }
+  read_exp(s0, k0);
+  // One stage.  sched_barrier: each part's reads and copies are issued beside its
+  // MFMAs, not in one run ahead of them.  A branch in here would let the compiler
+  // sink the MFMAs below it, so the last two stages are bodies of their own.
+  auto stage = [&](int64_t kb, auto next, auto next2) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      read(s1, kb, 1, i);
+      multiply(s0, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) s1.ea[i] = s0.ea[i];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) s1.eb[i] = s0.eb[i];
+    if constexpr (next) {
+      wait_vmcnt<0>();
+      __syncthreads();
+      read_exp(s0, kb + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (next2) fetch(kb + 2, i);
+      if constexpr (next) read(s0, kb + 1, 0, i);
+      multiply(s1, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int64_t kb = k0;
+  for (; kb + 2 < k1; ++kb) stage(kb, std::true_type{}, std::true_type{});
+  if (kb + 1 < k1) stage(kb++, std::true_type{}, std::false_type{});
+  stage(kb, std::false_type{}, std::false_type{});
+
+  // acc[i][k]: row (tm + wm FM + i) * 32 + (l & 31) of C, columns (tn + wn FN + k) * 32 + mfma32_row(v, l >> 5).
+  // 32 rows at a time go through LDS, so that a row's columns leave in 16-byte pieces.
+  T* C = static_cast<T*>(g.C) + (g.splits > 1 ? split * g.M * g.N : 0);
+  constexpr int kRow = FN * 32 * int(sizeof(T)) + 16;  // bytes of a row, and 16 to spread the banks
+  static_assert(TL::kWaves * 32 * kRow <= TL::kLds, "epilogue staging");
+  constexpr int kPer = 16 / int(sizeof(T)), kLanes = FN * 32 / kPer, kRows = 64 / kLanes;  // lanes of a row, rows at once
+  char* block = smem + w * (32 * kRow);
+  const int64_t n0 = (tn + wn * FN) * 32 + (l % kLanes) * kPer;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m0 = (tm + wm * FM + i) * 32;
 #pragma unroll
     for (int k = 0; k < FN; ++k)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t n = (tn + wn * FN + k) * 32 + mfma32_row(v, l >> 5);
-        if (n < g.N) {
-          T* c = C + m * g.N + n;
-          *c = from_f32<T>(g.accumulate ? to_f32<T>(*c) + acc[i][k][v] : acc[i][k][v]);
-        }
+      for (int v = 0; v < 16; v += 4) {
+        char* q = block + (l & 31) * kRow + (k * 32 + mfma32_row(v, l >> 5)) * int(sizeof(T));
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<u32x2*>(q) = u32x2{pack2bf(acc[i][k][v], acc[i][k][v + 1]), pack2bf(acc[i][k][v + 2], acc[i][k][v + 3])};
+        else
+          *reinterpret_cast<f32x4*>(q) = f32x4{acc[i][k][v], acc[i][k][v + 1], acc[i][k][v + 2], acc[i][k][v + 3]};
       }
+    // the block is this wave's own: its LDS operations complete in order
+#pragma unroll
+    for (int r = 0; r < 32; r += kRows) {
+      const int64_t m = m0 + r + l / kLanes;
+      if (m < g.M && n0 < g.N)
+        put16(C + m * g.N + n0, block + (r + l / kLanes) * kRow + (l % kLanes) * 16, g.N - n0, g.accumulate);
+    }
+  }
+}
+
+// C (+)= sum of the splits' partial sums, in order; no splits: zeros
+template <typename T>
+__global__ __launch_bounds__(256) void k_fp8_join(const float* part, int splits, T* C, int64_t n, int accumulate) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+    float s = 0.f;
+    for (int k = 0; k < splits; ++k) s += part[k * n + i];
+    C[i] = from_f32<T>(accumulate ? to_f32<T>(C[i]) + s : s);
   }
 }
 
 template <typename T>
-__global__ void k_fp8_zero(T* C, int64_t n) {
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) C[i] = from_f32<T>(0.f);
+void join_t(const float* part, int splits, T* C, int64_t n, int accumulate, hipStream_t s) {
+  hipLaunchKernelGGL(k_fp8_join<T>, dim3(uint32_t(std::min<int64_t>((n + 255) / 256, 4096))), dim3(256), 0, s, part,
+                     splits, C, n, accumulate);
+}
+
+// How a product is cut: 256 x 256 tiles where they fill the chip, else 128 x 128,
+// with K split into parts of 4 blocks at least while there are fewer tiles than CUs.
+struct Cut {
+  bool big;
+  int splits;
+  int64_t kb_per;
+};
+Cut cut(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kCus = 256;
+  const int64_t KB = (K + 127) / 128;
+  const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
+  Cut c;
+  c.big = tiles(256) >= kCus;
+  const int64_t want = c.big ? 1 : std::min(kCus / tiles(128), KB / 4);
+  c.kb_per = want > 1 ? (KB + want - 1) / want : KB;
+  c.splits = int((KB + c.kb_per - 1) / c.kb_per);
+  return c;
+}
+
+template <typename T, bool EXACT, int WM, int WN, int FM, int FN>
+void gemm_k(const GemmArgs& g, hipStream_t s) {
+  using TL = Tile<WM, WN, FM, FN>;
+  constexpr auto K = k_fp8_gemm<T, EXACT, WM, WN, FM, FN>;
+  const int64_t tiles = (g.A.RT + TL::kBM - 1) / TL::kBM * ((g.B.RT + TL::kBN - 1) / TL::kBN);
+  hipLaunchKernelGGL(K, dim3(uint32_t(tiles * g.splits)), dim3(TL::kThreads), (LdsLimit<K, TL::kLds>::bytes()), s, g);
 }
 
 template <typename T>
-void gemm_t(const GemmArgs& g, hipStream_t s) {
-  using TL = Tile<2, 2, 2, 2>;
-  constexpr auto K = k_fp8_gemm<T, 2, 2, 2, 2>;
-  const dim3 grid(uint32_t((g.A.RT + TL::kBM - 1) / TL::kBM * ((g.B.RT + TL::kBN - 1) / TL::kBN)));
-  hipLaunchKernelGGL(K, grid, dim3(TL::kThreads), (LdsLimit<K, TL::kLds>::bytes()), s, g);
+void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
+  constexpr bool kExact = sizeof(T) == 4;
+  if (c.splits > 1) {
+    T* C = static_cast<T*>(g.C);
+    const int accumulate = g.accumulate;
+    g.C = ws;
+    g.accumulate = 0;
+    gemm_k<float, kExact, 2, 2, 2, 2>(g, s);
+    join_t(ws, c.splits, C, g.M * g.N, accumulate, s);
+  } else if (c.big) {
+    gemm_k<T, kExact, 2, 2, 4, 4>(g, s);
+  } else {
+    gemm_k<T, kExact, 2, 2, 2, 2>(g, s);
+  }
 }
 
 template <typename T, bool ROWS, bool COLS>
@@ -439,24 +582,26 @@ void launch_fp8_unpack(const uint8_t* pk, void* X, int64_t rows, int64_t cols, i
     hipLaunchKernelGGL(k_fp8_unpack<float>, grid, dim3(256), 0, s, v, static_cast<float*>(X), rows, cols);
 }
 
-size_t fp8_gemm_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  const Cut c = cut(M, N, K);
+  return c.splits > 1 ? size_t(c.splits) * M * N * sizeof(float) : 0;
+}
 
 void launch_fp8_gemm(const uint8_t* A, const uint8_t* B, void* C, int accumulate, int64_t M, int64_t N, int64_t K,
-                     int bf16, float*, hipStream_t s) {
+                     int bf16, float* ws, hipStream_t s) {
   if (K == 0) {
-    if (accumulate) return;
-    const dim3 grid(uint32_t(std::min<int64_t>((M * N + 255) / 256, 4096)));
     if (bf16)
-      hipLaunchKernelGGL(k_fp8_zero<bf16_t>, grid, dim3(256), 0, s, static_cast<bf16_t*>(C), M * N);
+      join_t(ws, 0, static_cast<bf16_t*>(C), M * N, 0, s);
     else
-      hipLaunchKernelGGL(k_fp8_zero<float>, grid, dim3(256), 0, s, static_cast<float*>(C), M * N);
+      join_t(ws, 0, static_cast<float*>(C), M * N, accumulate, s);
     return;
   }
-  const GemmArgs g{View(A, M, K), View(B, N, K), C, M, N, accumulate};
+  const Cut c = cut(M, N, K);
+  const GemmArgs g{View(A, M, K), View(B, N, K), C, M, N, accumulate, c.splits, c.kb_per};
   if (bf16)
-    gemm_t<bf16_t>(g, s);
+    gemm_t<bf16_t>(g, c, ws, s);
   else
-    gemm_t<float>(g, s);
+    gemm_t<float>(g, c, ws, s);
 }
 
 }  // namespace mapl
