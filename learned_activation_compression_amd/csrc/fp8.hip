@@ -292,7 +292,7 @@ struct Tile {
   static constexpr int kStage = kUnits * 4096 + 512;   // codes, then 256 + 256 bytes of exponents
   static constexpr int kPieces = kUnits * 4 / kWaves;  // 1 KB pieces each wave copies per stage
   static constexpr int kLds = 2 * kStage;
-  static_assert(kUnits * 4 % kWaves == 0 && kPieces % 4 == 0 && kPieces % FM == 0 && (FM + FN) % FM == 0 && kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
+  static_assert(kUnits * 4 % kWaves == 0 && kPieces % 4 == 0 && kPieces % FM == 0 && kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
 };
 
 // One row of a wave's output block from LDS to C: 16 bytes per lane.
@@ -535,7 +535,7 @@ void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
     gemm_k<float, kExact, 2, 2, 2, 2>(g, s);
     join_t(ws, c.splits, C, g.M * g.N, accumulate, s);
   } else if (c.big) {
-    gemm_k<T, kExact, 2, 2, 4, 4>(g, s);
+    gemm_k<T, kExact, 2, 4, 4, 2>(g, s);
   } else {
     gemm_k<T, kExact, 2, 2, 2, 2>(g, s);
   }
