@@ -14,14 +14,12 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "vec8.h"
 
 namespace mapl {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 struct View {  // device view of a pack
   uint8_t* code = nullptr;
@@ -69,40 +67,12 @@ __device__ __forceinline__ u32x4 codes16(const float* v, float inv) {
   return u32x4{codes4(v, inv), codes4(v + 4, inv), codes4(v + 8, inv), codes4(v + 12, inv)};
 }
 
-// 16 consecutive elements, `left` of them in the row
-__device__ __forceinline__ void load16(const bf16_t* p, int64_t left, float* v) {
-  if (left >= 16) {
-    const u32x4 a = *reinterpret_cast<const u32x4_a2*>(p), b = *reinterpret_cast<const u32x4_a2*>(p + 8);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = __uint_as_float((i & 1) ? (a[i >> 1] & 0xffff0000u) : (a[i >> 1] << 16));
-      v[8 + i] = __uint_as_float((i & 1) ? (b[i >> 1] & 0xffff0000u) : (b[i >> 1] << 16));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < left ? bf2f(p[i]) : 0.f;
-  }
-}
-__device__ __forceinline__ void load16(const float* p, int64_t left, float* v) {
-  if (left >= 16) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const u32x4 a = *reinterpret_cast<const u32x4_a4*>(p + 4 * k);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * k + i] = __uint_as_float(a[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < left ? p[i] : 0.f;
-  }
-}
-
 // ---------------------------------------------------------------------- pack --
 // A block takes 128 rows x 128 columns of X.  Thread (i, j) = (tid / 8, tid % 8)
 // holds rows i + 32 k (k = 0..3), columns 16 j .. 16 j + 15.  The row operand
 // needs the sizes of 8 neighbouring lanes only.  The column operand goes through
 // LDS: wave w then holds rows 32 w .. 32 w + 31 of two columns per lane.
-template <typename T, bool ROWS, bool COLS>
+template <typename T, RowMode MODE, bool ROWS, bool COLS>
 __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, int square, int64_t R, int64_t C) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   T* tile = reinterpret_cast<T*>(smem);
@@ -112,10 +82,22 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
   const int64_t kb = blockIdx.x % nkb, rb = blockIdx.x / nkb;
   const int64_t c = kb * 128 + 16 * j;
   float v[4][16], am[4];
+  Fetch<T, MODE> f[4][2];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t r = rb * 128 + 32 * k + i0;
-    load16(X + r * C + c, r < R ? C - c : 0, v[k]);
+    const T* row = X + min(rb * 128 + 32 * k + i0, R - 1) * C;
+    f[k][0].issue(row, c, C);
+    f[k][1].issue(row, c + 8, C);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool in = rb * 128 + 32 * k + i0 < R;
+    const Raw8<T> lo = f[k][0].value(c, C, in), hi = f[k][1].value(c + 8, C, in);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[k][i] = lo.get(i);
+      v[k][8 + i] = hi.get(i);
+    }
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[k][i]));
@@ -296,27 +278,20 @@ struct Tile {
 };
 
 // One row of a wave's output block from LDS to C: 16 bytes per lane.
-__device__ __forceinline__ void put16(bf16_t* c, const char* src, int64_t left, int) {
+__device__ __forceinline__ void put16(bf16_t* c, const char* src, int left, int) {
   const u32x4 v = *reinterpret_cast<const u32x4*>(src);
-  if (left >= 8) {
-    *reinterpret_cast<u32x4_a2*>(c) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) c[i] = static_cast<bf16_t>(v[i >> 1] >> (16 * (i & 1)));
-  }
+  if (left >= 8)
+    st8_any(c, v);
+  else
+    st_tail(c, v, left);
 }
-__device__ __forceinline__ void put16(float* c, const char* src, int64_t left, int accumulate) {
+__device__ __forceinline__ void put16(float* c, const char* src, int left, int accumulate) {
   f32x4 v = *reinterpret_cast<const f32x4*>(src);
-  typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-  if (left >= 4) {
-    if (accumulate) v += *reinterpret_cast<const f32x4_a4*>(c);
-    *reinterpret_cast<f32x4_a4*>(c) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) c[i] = accumulate ? c[i] + v[i] : v[i];
-  }
+  if (accumulate) v += __builtin_bit_cast(f32x4, left >= 4 ? ld16B(c) : ld_tail4(c, left));
+  if (left >= 4)
+    st16B(c, __builtin_bit_cast(u32x4, v));
+  else
+    st_tail4(c, __builtin_bit_cast(u32x4, v), left);
 }
 
 // The loop runs one stage (128 columns) ahead in LDS and one step (64 columns)
@@ -476,7 +451,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
     for (int r = 0; r < 32; r += kRows) {
       const int64_t m = m0 + r + l / kLanes;
       if (m < g.M && n0 < g.N)
-        put16(C + m * g.N + n0, block + (r + l / kLanes) * kRow + (l % kLanes) * 16, g.N - n0, g.accumulate);
+        put16(C + m * g.N + n0, block + (r + l / kLanes) * kRow + (l % kLanes) * 16, static_cast<int>(g.N - n0), g.accumulate);
     }
   }
 }
@@ -541,12 +516,16 @@ void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
   }
 }
 
-template <typename T, bool ROWS, bool COLS>
-void pack_k(const T* X, uint8_t* pk, uint8_t* pkT, int square, int64_t R, int64_t C, hipStream_t s) {
-  constexpr auto K = k_fp8_pack<T, ROWS, COLS>;
+template <typename T, RowMode MODE, bool ROWS, bool COLS>
+void pack_m(const T* X, uint8_t* pk, uint8_t* pkT, int square, int64_t R, int64_t C, hipStream_t s) {
+  constexpr auto K = k_fp8_pack<T, MODE, ROWS, COLS>;
   constexpr int kTile = COLS ? int(128 * 130 * sizeof(T)) : 16;
   hipLaunchKernelGGL(K, dim3(uint32_t((C + 127) / 128 * ((R + 127) / 128))), dim3(256), (LdsLimit<K, kTile>::bytes()), s,
                      X, View(pk, R, C), View(pkT, C, R), square, R, C);
+}
+template <typename T, bool ROWS, bool COLS>
+void pack_k(const T* X, uint8_t* pk, uint8_t* pkT, int square, int64_t R, int64_t C, hipStream_t s) {
+  by_row_mode<T, true>(C, {X}, [&](auto m) { pack_m<T, decltype(m)::value, ROWS, COLS>(X, pk, pkT, square, R, C, s); });
 }
 template <typename T>
 void pack_t(const T* X, uint8_t* pk, uint8_t* pkT, int square, int64_t R, int64_t C, hipStream_t s) {

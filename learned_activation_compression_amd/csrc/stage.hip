@@ -3,77 +3,13 @@
 // backward pass.  Formulas: include/mapl_stage.h.  All of it is bound by memory
 // traffic: every tensor is read or written once, rows stay in registers between
 // their sums and their use.
+#include <type_traits>
+
 #include "internal.h"
+#include "vec8.h"
 
 namespace mapl {
 namespace {
-
-// ------------------------------------------------------ 8 elements of a row --
-// A thread moves 8 consecutive elements.  The vector types ask only for the
-// alignment of an element, so rows of any width and tensors of any offset take
-// the same 16-byte accesses; only a row's last elements go one by one.
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-
-template <typename T>
-struct Raw8;  // 8 elements as loaded
-template <>
-struct Raw8<bf16_t> {
-  u32x4 a;
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t w = a[i >> 1];
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
-  }
-  __device__ __forceinline__ void load(const bf16_t* p, int left) {
-    if (left >= 8) {
-      a = *reinterpret_cast<const u32x4_a2*>(p);
-    } else {
-      a = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) a[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-    }
-  }
-};
-template <>
-struct Raw8<float> {
-  u32x4 a, b;
-  __device__ __forceinline__ float get(int i) const { return __uint_as_float(i < 4 ? a[i & 3] : b[i & 3]); }
-  __device__ __forceinline__ void load(const float* p, int left) {
-    if (left >= 8) {
-      a = *reinterpret_cast<const u32x4_a4*>(p);
-      b = *reinterpret_cast<const u32x4_a4*>(p + 4);
-    } else {
-      a = b = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) (i < 4 ? a : b)[i & 3] = __float_as_uint(p[i]);
-    }
-  }
-};
-
-__device__ __forceinline__ void store8(bf16_t* p, const float* v, int left) {
-  if (left >= 8) {
-    *reinterpret_cast<u32x4_a2*>(p) =
-        u32x4{pack2bf(v[0], v[1]), pack2bf(v[2], v[3]), pack2bf(v[4], v[5]), pack2bf(v[6], v[7])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = f2bf(v[i]);
-  }
-}
-__device__ __forceinline__ void store8(float* p, const float* v, int left) {
-  if (left >= 8) {
-    *reinterpret_cast<u32x4_a4*>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                            __float_as_uint(v[3])};
-    *reinterpret_cast<u32x4_a4*>(p + 4) = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                                                __float_as_uint(v[7])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = v[i];
-  }
-}
 
 // ----------------------------------------------------------------- generator --
 struct Drop {
@@ -125,38 +61,37 @@ Drop make_drop(double p, uint64_t seed, uint64_t offset) {
 // Units of 8 columns, unit u = row * nb + column / 8.
 constexpr int kDropUnits = 4;  // units in flight per thread
 
-template <typename T>
+template <typename T, RowMode MODE>
 __global__ __launch_bounds__(256) void k_dropout(const T* X, T* Y, Drop dr, int64_t units, uint32_t nb, int64_t d) {
   const int64_t u0 = int64_t(blockIdx.x) * (256 * kDropUnits) + threadIdx.x;
-  int64_t row = u0 / nb;
-  uint32_t b = static_cast<uint32_t>(u0 - row * nb);
+  int64_t row[kDropUnits];
+  uint32_t b[kDropUnits], keep[kDropUnits];
+  row[0] = u0 / nb;
+  b[0] = static_cast<uint32_t>(u0 - row[0] * nb);
   const uint32_t step_row = 256 / nb, step_b = 256 % nb;
-  Raw8<T> x[kDropUnits];
-  int64_t at[kDropUnits];
-  uint32_t keep[kDropUnits];
-  int left[kDropUnits];
+  Fetch<T, MODE> x[kDropUnits];
+#pragma unroll
+  for (int k = 0; k < kDropUnits; ++k) {
+    if (k > 0) {
+      row[k] = row[k - 1] + step_row;
+      b[k] = b[k - 1] + step_b;
+      if (b[k] >= nb) {
+        b[k] -= nb;
+        ++row[k];
+      }
+    }
+    x[k].issue(X + (u0 + k * 256 < units ? row[k] : 0) * d, int64_t(b[k]) * 8, d);
+  }
+#pragma unroll
+  for (int k = 0; k < kDropUnits; ++k) keep[k] = keep8(dr, b[k], static_cast<uint64_t>(row[k]));
 #pragma unroll
   for (int k = 0; k < kDropUnits; ++k) {
     const bool in = u0 + k * 256 < units;
-    at[k] = row * d + int64_t(b) * 8;
-    left[k] = in ? static_cast<int>(min(d - int64_t(b) * 8, int64_t(8))) : 0;
-    if (in) x[k].load(X + at[k], left[k]);
-    keep[k] = keep8(dr, b, static_cast<uint64_t>(row));
-    b += step_b;
-    row += step_row;
-    if (b >= nb) {
-      b -= nb;
-      ++row;
-    }
-  }
+    const Raw8<T> r = x[k].value(int64_t(b[k]) * 8, d, in);
+    float v[8];
 #pragma unroll
-  for (int k = 0; k < kDropUnits; ++k) {
-    if (left[k] > 0) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = (keep[k] >> i) & 1 ? x[k].get(i) * dr.scale : 0.f;
-      store8(Y + at[k], v, left[k]);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = (keep[k] >> i) & 1 ? r.get(i) * dr.scale : 0.f;
+    put_row<MODE>(Y + row[k] * d, int64_t(b[k]) * 8, d, in, v);
   }
 }
 
@@ -167,20 +102,51 @@ __global__ __launch_bounds__(256) void k_dropout(const T* X, T* Y, Drop dr, int6
 template <int TPR>
 constexpr int kBlock = TPR > 256 ? TPR : 256;
 
-template <int TPR>
-__device__ __forceinline__ float slot_sum(float v, float* lds) {
-#pragma unroll
-  for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) v += __shfl_xor(v, m);
-  if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) v += lds[w];
+// Sum over the lanes of a slot (or of its wave), the same value and order in
+// every lane: data-parallel primitives within 16 lanes, lane swaps beyond.
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+  static_assert(L == 16 || L == 32 || L == 64, "lanes");
+  const auto dpp = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});   // lanes 1 0 3 2 of a quad
+  v += dpp(v, std::integral_constant<int, 0x4E>{});   // lanes 2 3 0 1 of a quad
+  v += dpp(v, std::integral_constant<int, 0x141>{});  // 8 lanes mirrored
+  v += dpp(v, std::integral_constant<int, 0x140>{});  // 16 lanes mirrored
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
   return v;
+}
+
+// K sums over a slot at once.  A slot of several waves exchanges them through
+// lds[2][K][16]; `turn` alternates its halves, so that one barrier is enough.
+template <int TPR, int K>
+__device__ __forceinline__ void slot_sums(float (&v)[K], float* lds, int& turn) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = lane_sum<(TPR < 64 ? TPR : 64)>(v[k]);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    float* at = lds + (turn & 1) * (3 * 16);
+    ++turn;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) at[k * 16 + (threadIdx.x >> 6)] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[k] += at[k * 16 + threadIdx.x / TPR * W + w];
+    }
+  }
 }
 
 template <typename T>
@@ -193,60 +159,74 @@ struct NormArgs {
   int d;
 };
 
-template <typename T, int TPR, int V>
+template <typename T, int TPR, int V, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
-  __shared__ float lds[16];
+  __shared__ float lds[2 * 3 * 16];
+  int turn = 0;
   const int l = threadIdx.x % TPR;
-  // every thread of a block takes the same number of turns (slot_sum has barriers)
+  const auto col = [&](int j) { return 8 * (j * TPR + l); };
+  // every thread of a block takes the same number of turns (slot_sums has barriers)
   for (int64_t n0 = int64_t(blockIdx.x) * S; n0 < a.N; n0 += int64_t(gridDim.x) * S) {
     const int64_t n = n0 + threadIdx.x / TPR;
     const bool in = n < a.N;
-    Raw8<T> rx[V], ry[V];
-    int left[V];
+    const int64_t at = (in ? n : 0) * a.d;
+    Fetch<T, MODE> fx[V], fy[V], fq[V], fg[V], fw[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = 8 * (j * TPR + l);
-      left[j] = in ? a.d - c : 0;
-      rx[j].load(a.X + n * a.d + c, left[j]);
-      if (a.Y) ry[j].load(a.Y + n * a.d + c, left[j]);
+    for (int j = 0; j < V; ++j) fx[j].issue(a.X + at, col(j), a.d);
+    if (a.Y) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) fy[j].issue(a.Y + at, col(j), a.d);
+    }
+    if (a.w_post) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) fq[j].issue(a.w_post, col(j), a.d);
+    }
+    if (a.gate) {
+      const T* g = a.gate + (in ? n / a.rows_per_gate : 0) * a.d;
+#pragma unroll
+      for (int j = 0; j < V; ++j) fg[j].issue(g, col(j), a.d);
+    }
+    if (a.H) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) fw[j].issue(a.w_pre, col(j), a.d);
     }
     float x[V][8];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+      const Raw8<T> r = fx[j].value(col(j), a.d, in);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = a.res_scale * rx[j].get(i);
+      for (int i = 0; i < 8; ++i) x[j][i] = a.res_scale * r.get(i);
+    }
     if (a.Y) {
-      float u[V][8], s = 0.f;
+      float u[V][8], s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < V; ++j) {
+        const Raw8<T> r = fy[j].value(col(j), a.d, in);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[j][i] = ry[j].get(i);
+        for (int i = 0; i < 8; ++i) u[j][i] = r.get(i);
         if (a.dr.t) {
           const uint32_t keep = keep8(a.dr, static_cast<uint32_t>(j * TPR + l), static_cast<uint64_t>(n));
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[j][i] = (keep >> i) & 1 ? u[j][i] * a.dr.scale : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += u[j][i] * u[j][i];
+        for (int i = 0; i < 8; ++i) s[0] += u[j][i] * u[j][i];
       }
       if (a.w_post) {
-        s = slot_sum<TPR>(s, lds);
-        const float q = rsqrtf(s * a.inv_d + a.eps);
+        slot_sums<TPR>(s, lds, turn);
+        const float q = rsqrtf(s[0] * a.inv_d + a.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          Raw8<T> w;
-          w.load(a.w_post + 8 * (j * TPR + l), left[j]);
+          const Raw8<T> w = fq[j].value(col(j), a.d, true);
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[j][i] *= q * w.get(i);
         }
       }
       if (a.gate) {
-        const T* g = a.gate + (in ? n / a.rows_per_gate : 0) * a.d;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          Raw8<T> w;
-          w.load(g + 8 * (j * TPR + l), left[j]);
+          const Raw8<T> w = fg[j].value(col(j), a.d, true);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[j][i] += w.get(i) * u[j][i];
         }
@@ -259,23 +239,22 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
     }
     if (a.X_out) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) store8(a.X_out + n * a.d + 8 * (j * TPR + l), x[j], left[j]);
+      for (int j = 0; j < V; ++j) put_row<MODE>(a.X_out + at, col(j), a.d, in, x[j]);
     }
     if (a.H) {
-      float s = 0.f;
+      float s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += i < left[j] ? x[j][i] * x[j][i] : 0.f;
-      s = slot_sum<TPR>(s, lds);
-      const float r = rsqrtf(s * a.inv_d + a.eps);
+        for (int i = 0; i < 8; ++i) s[0] += col(j) + i < a.d ? x[j][i] * x[j][i] : 0.f;
+      slot_sums<TPR>(s, lds, turn);
+      const float r = rsqrtf(s[0] * a.inv_d + a.eps);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        Raw8<T> w;
-        w.load(a.w_pre + 8 * (j * TPR + l), left[j]);
+        const Raw8<T> w = fw[j].value(col(j), a.d, true);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[j][i] *= r * w.get(i);
-        store8(a.H + n * a.d + 8 * (j * TPR + l), x[j], left[j]);
+        put_row<MODE>(a.H + at, col(j), a.d, in, x[j]);
       }
     }
   }
@@ -306,14 +285,17 @@ struct NormBwdArgs {
   int d, accumulate;
 };
 
-template <typename T, int TPR, int V>
+// PRE: with gH and X_out; POST: with Y; MANY: many gate rows.  The loads of the
+// next row are in flight over the arithmetic of this one.
+template <typename T, int TPR, int V, bool PRE, bool POST, bool MANY, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
-  __shared__ float lds[16];
+  __shared__ float lds[2 * 3 * 16];
   __shared__ float acc_lds[S > 1 ? 256 * 8 : 1];
+  int turn = 0;
   const int l = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   int64_t r0, r1, turns;  // this slot's rows; the block's turns
-  if (a.sp.many) {
+  if constexpr (MANY) {
     const int64_t g0 = (int64_t(blockIdx.x) * S + slot) * a.sp.gps;
     r0 = min(g0 * a.rows_per_gate, a.N);
     r1 = min((g0 + a.sp.gps) * a.rows_per_gate, a.N);
@@ -326,155 +308,156 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a
     r0 = min(b0 + slot * turns, b1);
     r1 = min(b0 + (slot + 1) * turns, b1);
   }
-  float Q[V][8], Wp[V][8], Hp[V][8];
+  const bool norm = a.w_post != nullptr;
+  const auto col = [&](int j) { return 8 * (j * TPR + l); };
+  const auto weight = [&](Raw8<T>& w, const T* p, int j) {
+    Fetch<T, MODE> f;
+    f.issue(p, col(j), a.d);
+    w = f.value(col(j), a.d, true);
+  };
+  // the weights stay in registers; an absent one is 1
+  Raw8<T> wq[V], wp[V], wg[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    wp[j].ones();
+    wg[j].ones();
+    if constexpr (PRE) weight(wq[j], a.w_pre, j);
+    if (POST && norm) weight(wp[j], a.w_post, j);
+    if (POST && !MANY && a.gate) weight(wg[j], a.gate + blockIdx.x / a.sp.bpg * a.d, j);
+  }
+  struct Row {
+    Fetch<T, MODE> t[V], h[V], x[V], y[V], g[V];
+  };
+  const T* gxo = a.gX_out ? a.gX_out : a.gH;  // without gX_out: read something, use zero
+  const bool has_t = a.gX_out != nullptr;
+  const auto load = [&](Row& r, int64_t n) {
+    const bool in = n < r1;
+    const int64_t at = (in ? n : 0) * a.d;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      r.t[j].issue(gxo + at, col(j), a.d);
+      if constexpr (PRE) r.h[j].issue(a.gH + at, col(j), a.d);
+      if constexpr (PRE) r.x[j].issue(a.X_out + at, col(j), a.d);
+      if constexpr (POST) r.y[j].issue(a.Y + at, col(j), a.d);
+      if constexpr (MANY) r.g[j].issue(a.gate + (in ? n / a.rows_per_gate : 0) * a.d, col(j), a.d);
+    }
+  };
+  float Q[V][8], Wp[V][8], Hp[V][8];  // sums over rows of t q u (this gate row's), gate t q u (MANY), gH r X_out
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) Q[j][i] = Wp[j][i] = Hp[j][i] = 0.f;
 
+  Row cur, nxt;
+  load(cur, r0);
   for (int64_t k = 0; k < turns; ++k) {
     const int64_t n = r0 + k;
     const bool in = n < r1;
-    const int64_t gate_row = a.gate && in ? n / a.rows_per_gate : 0;
-    float t[V][8], u[V][8];
-    Raw8<T> rx[V], rh[V];
+    load(nxt, n + 1 < r0 + turns ? n + 1 : r1);
+    float t[V][8], u[V][8], s[3] = {0.f, 0.f, 0.f};
     uint32_t keep[V];
-    int left[V];
-    float sx = 0.f, sax = 0.f, su = 0.f;
+    Raw8<T> rt[V], rh[V], rx[V], rg[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int c = 8 * (j * TPR + l);
-      left[j] = in ? a.d - c : 0;
-      Raw8<T> v;
-      if (a.gX_out) {
-        v.load(a.gX_out + n * a.d + c, left[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[j][i] = v.get(i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[j][i] = 0.f;
-      }
-      if (a.gH) {
-        rx[j].load(a.X_out + n * a.d + c, left[j]);
-        rh[j].load(a.gH + n * a.d + c, left[j]);
-        v.load(a.w_pre + c, left[j]);
+      rt[j] = cur.t[j].value(col(j), a.d, in);
+      if constexpr (PRE) {
+        rh[j] = cur.h[j].value(col(j), a.d, in);
+        rx[j] = cur.x[j].value(col(j), a.d, in);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          sx += rx[j].get(i) * rx[j].get(i);
-          sax += rh[j].get(i) * v.get(i) * rx[j].get(i);
+          s[0] += rx[j].get(i) * rx[j].get(i);
+          s[1] += rh[j].get(i) * wq[j].get(i) * rx[j].get(i);
         }
       }
-      keep[j] = 0xffu;
-      if (a.Y) {
-        v.load(a.Y + n * a.d + c, left[j]);
+      if constexpr (MANY) rg[j] = cur.g[j].value(col(j), a.d, in);
+      if constexpr (POST) {
+        const Raw8<T> ry = cur.y[j].value(col(j), a.d, in);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[j][i] = v.get(i);
+        for (int i = 0; i < 8; ++i) u[j][i] = ry.get(i);
+        keep[j] = 0xffu;
         if (a.dr.t) {
           keep[j] = keep8(a.dr, static_cast<uint32_t>(j * TPR + l), static_cast<uint64_t>(n));
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[j][i] = (keep[j] >> i) & 1 ? u[j][i] * a.dr.scale : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) su += u[j][i] * u[j][i];
+        for (int i = 0; i < 8; ++i) s[2] += u[j][i] * u[j][i];
       }
     }
-    if (a.gH) {
-      sx = slot_sum<TPR>(sx, lds);
-      sax = slot_sum<TPR>(sax, lds);
-      const float r = rsqrtf(sx * a.inv_d + a.eps), m = sax * a.inv_d * r * r;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        Raw8<T> w;
-        w.load(a.w_pre + 8 * (j * TPR + l), left[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          t[j][i] += r * (rh[j].get(i) * w.get(i) - rx[j].get(i) * m);
-          Hp[j][i] += rh[j].get(i) * (r * rx[j].get(i));
-        }
-      }
-    }
+    slot_sums<TPR>(s, lds, turn);
+    const float r = rsqrtf(s[0] * a.inv_d + a.eps), m = s[1] * a.inv_d * r * r;
+    const float q = norm ? rsqrtf(s[2] * a.inv_d + a.eps) : 1.f;
+    float sb[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = a.res_scale * t[j][i];
-      store8(a.gX + n * a.d + 8 * (j * TPR + l), v, left[j]);
-    }
-    if (a.Y) {
-      float q = 1.f, sb = 0.f;
-      if (a.w_post) q = rsqrtf(slot_sum<TPR>(su, lds) * a.inv_d + a.eps);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c = 8 * (j * TPR + l);
-        Raw8<T> w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {
+        t[j][i] = has_t ? rt[j].get(i) : 0.f;
+        if constexpr (PRE) {
+          t[j][i] += r * (rh[j].get(i) * wq[j].get(i) - rx[j].get(i) * m);
+          Hp[j][i] += rh[j].get(i) * (r * rx[j].get(i));
+        }
+        v[i] = a.res_scale * t[j][i];
+        if constexpr (POST) {
           u[j][i] *= q;
           Q[j][i] += t[j][i] * u[j][i];
-        }
-        if (a.gate) {
-          w.load(a.gate + gate_row * a.d + c, left[j]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[j][i] *= w.get(i);
-        }
-        if (a.w_post) {
-          w.load(a.w_post + c, left[j]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            t[j][i] *= w.get(i);
-            sb += t[j][i] * u[j][i];
-          }
+          t[j][i] *= (MANY ? rg[j] : wg[j]).get(i) * wp[j].get(i);
+          sb[0] += t[j][i] * u[j][i];
         }
       }
-      const float m = a.w_post ? slot_sum<TPR>(sb, lds) * a.inv_d : 0.f;
+      put_row<MODE>(a.gX + n * a.d, col(j), a.d, in, v);
+    }
+    if constexpr (POST) {
+      slot_sums<TPR>(sb, lds, turn);
+      const float mb = norm ? sb[0] * a.inv_d : 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = q * (t[j][i] - u[j][i] * m);
+          v[i] = q * (t[j][i] - u[j][i] * mb);
           if (a.dr.t) v[i] = (keep[j] >> i) & 1 ? v[i] * a.dr.scale : 0.f;
         }
-        store8(a.gY + n * a.d + 8 * (j * TPR + l), v, left[j]);
+        put_row<MODE>(a.gY + n * a.d, col(j), a.d, in, v);
       }
-    }
-    // the last row of a gate row (or of this slot): its sum goes to the weights
-    if (in && (n + 1 == r1 || (a.sp.many && (n + 1) % a.rows_per_gate == 0))) {
+      // the last row of a gate row: its gradient is whole, and its part of w_post's
+      if constexpr (MANY) {
+        if (in && (n + 1) % a.rows_per_gate == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c = 8 * (j * TPR + l);
-        Raw8<T> wg, wp;
-        if (a.gate) wg.load(a.gate + gate_row * a.d + c, left[j]);
-        if (a.w_post) wp.load(a.w_post + c, left[j]);
+          for (int j = 0; j < V; ++j) {
+            const int c = 8 * (j * TPR + l), left = a.d - c;
+            float* g = a.g_gate + n / a.rows_per_gate * a.d + c;
+            float v[8];
+            Raw8<float> old;
+            if (a.accumulate) load8(old, g, left);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          Wp[j][i] += a.gate ? wg.get(i) * Q[j][i] : Q[j][i];
-          if (a.w_post) Q[j][i] *= wp.get(i);
-        }
-        if (a.sp.many) {
-          float* g = a.g_gate + gate_row * a.d + c;
-          float v[8];
-          Raw8<float> old;
-          if (a.accumulate) old.load(g, left[j]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] = a.accumulate ? old.get(i) + Q[j][i] : Q[j][i];
-            Q[j][i] = 0.f;
+            for (int i = 0; i < 8; ++i) {
+#pragma clang fp contract(off)  // accumulating adds the gradient that is written otherwise
+              Wp[j][i] += rg[j].get(i) * Q[j][i];
+              v[i] = wp[j].get(i) * Q[j][i];
+              if (a.accumulate) v[i] += old.get(i);
+              Q[j][i] = 0.f;
+            }
+            store8(g, v, left);
           }
-          store8(g, v, left[j]);
         }
       }
     }
+    cur = nxt;
   }
   // the block's partial rows: its slots' sums in slot order
 #pragma unroll
   for (int which = 0; which < 3; ++which) {
-    if (which == 0 ? a.w_post == nullptr : which == 1 ? (a.gate == nullptr || a.sp.many) : a.gH == nullptr) continue;
+    if (which == 0 ? !POST || !norm : which == 1 ? !POST || MANY || !a.gate : !PRE) continue;
     float* out = a.part + (which * a.sp.blocks + blockIdx.x) * a.d;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float* v = which == 0 ? Wp[j] : which == 1 ? Q[j] : Hp[j];
       const int c = 8 * (j * TPR + l);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = which == 2 ? Hp[j][i] : MANY ? Wp[j][i] : Q[j][i] * (which == 0 ? wg[j] : wp[j]).get(i);
       if constexpr (S == 1) {
         store8(out + c, v, a.d - c);
       } else {
@@ -492,28 +475,43 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a
   }
 }
 
-// Joins the partial rows: block (x, y) sums 16 columns of one output row, 16
-// threads a column, in a fixed order.  y = 0: w_post; 1: w_pre; 2 + g: gate row g.
+// Joins the partial rows: block (x, y) sums 32 columns of one output row, 4
+// columns by 32 runs of rows a thread, in a fixed order.  y = 0: w_post; 1:
+// w_pre; 2 + g: gate row g.
 __global__ __launch_bounds__(256) void k_stage_norm_grads(const float* part, float* g_w_post, float* g_w_pre,
                                                           float* g_gate, int64_t blocks, int64_t bpg, int d,
                                                           int accumulate) {
-  __shared__ float lds[16][17];
+  __shared__ float lds[32][33];
   const int64_t y = int64_t(blockIdx.y);
   float* out = y == 0 ? g_w_post : y == 1 ? g_w_pre : g_gate ? g_gate + (y - 2) * d : nullptr;
   if (out == nullptr) return;
   const float* src = part + (y == 0 ? 0 : y == 1 ? 2 * blocks : blocks + (y - 2) * bpg) * d;
   const int64_t rows = y < 2 ? blocks : bpg;
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, c = blockIdx.x * 16 + cx;
-  float s = 0.f;
-  if (c < d)
-    for (int64_t r = ry; r < rows; r += 16) s += src[r * d + c];
-  lds[ry][cx] = s;
-  __syncthreads();
-  if (ry == 0 && c < d) {
-    s = 0.f;
+  const int cx = (threadIdx.x & 7) * 4, ry = threadIdx.x >> 3, c = blockIdx.x * 32 + cx;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c + 4 <= d) {
+#pragma unroll 8
+    for (int64_t r = ry; r < rows; r += 32) {
+      const u32x4 v = ld16B(src + r * d + c);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += lds[k][cx];
-    out[c] = accumulate ? out[c] + s : s;
+      for (int i = 0; i < 4; ++i) s[i] += __uint_as_float(v[i]);
+    }
+  } else {
+    for (int64_t r = ry; r < rows; r += 32)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < d) s[i] += src[r * d + c + i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) lds[ry][cx + i] = s[i];
+  __syncthreads();
+  const int e = threadIdx.x;
+  if (e < 32 && blockIdx.x * 32 + e < static_cast<uint32_t>(d)) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v += lds[k][e];
+    out += blockIdx.x * 32 + e;
+    *out = accumulate ? *out + v : v;
   }
 }
 
@@ -524,12 +522,13 @@ struct SlotShape {
   int tpr, v;
 };
 int slots_per_block(SlotShape s) { return s.tpr > 256 ? 1 : 256 / s.tpr; }
-SlotShape slot_shape(int64_t d) {
-  if (d <= 64) return {8, 1};
+SlotShape slot_shape(int64_t d, bool bwd) {
   if (d <= 128) return {16, 1};
   if (d <= 256) return {32, 1};
   if (d <= 512) return {64, 1};
-  if (d <= 1024) return {64, 2};
+  // two vectors a thread and no barriers, but half the waves: better forward (16384 x 1024 bf16: 27.6 against
+  // 33.2 us), worse backward (46.0 against 43.1 us), where a row takes 240 registers that way
+  if (d <= 1024) return bwd ? SlotShape{128, 1} : SlotShape{64, 2};
   if (d <= 2048) return {256, 1};
   if (d <= 4096) return {512, 1};
   return {1024, 1};
@@ -537,7 +536,7 @@ SlotShape slot_shape(int64_t d) {
 
 BwdSplit bwd_split(int64_t N, int64_t d, int64_t gate_rows) {
   BwdSplit s{};
-  const int64_t S = slots_per_block(slot_shape(d)), G = gate_rows > 0 ? gate_rows : 1, rpg = N / G;
+  const int64_t S = slots_per_block(slot_shape(d, true)), G = gate_rows > 0 ? gate_rows : 1, rpg = N / G;
   s.many = G > kBwdBlocks;
   if (s.many) {
     s.gps = (G + kBwdBlocks * S - 1) / (kBwdBlocks * S);
@@ -550,29 +549,41 @@ BwdSplit bwd_split(int64_t N, int64_t d, int64_t gate_rows) {
   return s;
 }
 
-template <typename T, template <typename, int, int> class L, typename A>
+template <typename T, template <typename, int, int> class L, bool BWD, typename A>
 void by_shape(SlotShape sh, const A& args, dim3 grid, hipStream_t s) {
-  switch (sh.tpr * 16 + sh.v) {
-    case 8 * 16 + 1: return L<T, 8, 1>::go(args, grid, s);
-    case 16 * 16 + 1: return L<T, 16, 1>::go(args, grid, s);
-    case 32 * 16 + 1: return L<T, 32, 1>::go(args, grid, s);
-    case 64 * 16 + 1: return L<T, 64, 1>::go(args, grid, s);
-    case 64 * 16 + 2: return L<T, 64, 2>::go(args, grid, s);
-    case 256 * 16 + 1: return L<T, 256, 1>::go(args, grid, s);
-    case 512 * 16 + 1: return L<T, 512, 1>::go(args, grid, s);
-    default: return L<T, 1024, 1>::go(args, grid, s);
+  if (sh.tpr == 16) return L<T, 16, 1>::go(args, grid, s);
+  if (sh.tpr == 32) return L<T, 32, 1>::go(args, grid, s);
+  if constexpr (BWD) {
+    if (sh.tpr == 128) return L<T, 128, 1>::go(args, grid, s);
+  } else {
+    if (sh.tpr == 64 && sh.v == 2) return L<T, 64, 2>::go(args, grid, s);
   }
+  if (sh.tpr == 64) return L<T, 64, 1>::go(args, grid, s);
+  if (sh.tpr == 256) return L<T, 256, 1>::go(args, grid, s);
+  if (sh.tpr == 512) return L<T, 512, 1>::go(args, grid, s);
+  return L<T, 1024, 1>::go(args, grid, s);
 }
 template <typename T, int TPR, int V>
 struct FwdLaunch {
   static void go(const NormArgs<T>& a, dim3 grid, hipStream_t s) {
-    hipLaunchKernelGGL((k_stage_norm<T, TPR, V>), grid, dim3(kBlock<TPR>), 0, s, a);
+    by_row_mode<T, TPR == 16>(a.d, {a.X, a.Y, a.w_post, a.gate, a.w_pre, a.X_out, a.H}, [&](auto m) {
+      hipLaunchKernelGGL((k_stage_norm<T, TPR, V, decltype(m)::value>), grid, dim3(kBlock<TPR>), 0, s, a);
+    });
   }
 };
 template <typename T, int TPR, int V>
 struct BwdLaunch {
+  template <bool PRE, bool POST, bool MANY>
+  static void k(const NormBwdArgs<T>& a, dim3 grid, hipStream_t s) {
+    by_row_mode<T, TPR == 16>(a.d, {a.gX_out, a.gH, a.X_out, a.Y, a.w_post, a.gate, a.w_pre, a.gX, a.gY}, [&](auto m) {
+      hipLaunchKernelGGL((k_stage_norm_bwd<T, TPR, V, PRE, POST, MANY, decltype(m)::value>), grid, dim3(kBlock<TPR>), 0,
+                         s, a);
+    });
+  }
   static void go(const NormBwdArgs<T>& a, dim3 grid, hipStream_t s) {
-    hipLaunchKernelGGL((k_stage_norm_bwd<T, TPR, V>), grid, dim3(kBlock<TPR>), 0, s, a);
+    if (!a.Y) return k<true, false, false>(a, grid, s);
+    if (a.sp.many) return a.gH ? k<true, true, true>(a, grid, s) : k<false, true, true>(a, grid, s);
+    return a.gH ? k<true, true, false>(a, grid, s) : k<false, true, false>(a, grid, s);
   }
 };
 
@@ -582,8 +593,10 @@ template <typename T>
 static void dropout_t(const void* X, void* Y, double p, uint64_t seed, uint64_t offset, int64_t N, int64_t d,
                       hipStream_t s) {
   const int64_t nb = (d + 7) / 8, units = N * nb, per = 256 * kDropUnits;
-  hipLaunchKernelGGL(k_dropout<T>, dim3(uint32_t((units + per - 1) / per)), dim3(256), 0, s,
-                     static_cast<const T*>(X), static_cast<T*>(Y), make_drop(p, seed, offset), units, uint32_t(nb), d);
+  by_row_mode<T, true>(d, {X, Y}, [&](auto m) {
+    hipLaunchKernelGGL((k_dropout<T, decltype(m)::value>), dim3(uint32_t((units + per - 1) / per)), dim3(256), 0, s,
+                       static_cast<const T*>(X), static_cast<T*>(Y), make_drop(p, seed, offset), units, uint32_t(nb), d);
+  });
 }
 
 void launch_dropout(const void* X, void* Y, double p, uint64_t seed, uint64_t offset, int64_t N, int64_t d, int bf16,
@@ -608,10 +621,10 @@ static void norm_t(const StageNorm& c, hipStream_t s) {
   a.N = c.N;
   a.rows_per_gate = c.gate_rows > 0 ? c.N / c.gate_rows : c.N;
   a.d = int(c.d);
-  const SlotShape sh = slot_shape(c.d);
+  const SlotShape sh = slot_shape(c.d, false);
   const int64_t S = slots_per_block(sh);
   const uint32_t grid = uint32_t(std::min<int64_t>((c.N + S - 1) / S, 256 * 8));
-  by_shape<T, FwdLaunch>(sh, a, dim3(grid), s);
+  by_shape<T, FwdLaunch, false>(sh, a, dim3(grid), s);
 }
 
 void launch_stage_norm(const StageNorm& c, int bf16, hipStream_t s) { (bf16 ? norm_t<bf16_t> : norm_t<float>)(c, s); }
@@ -643,10 +656,10 @@ static void norm_bwd_t(const StageNorm& c, const StageNormGrads& g, hipStream_t 
   a.rows_per_gate = c.gate_rows > 0 ? c.N / c.gate_rows : c.N;
   a.d = int(c.d);
   a.accumulate = g.accumulate;
-  by_shape<T, BwdLaunch>(slot_shape(c.d), a, dim3(uint32_t(a.sp.blocks)), s);
+  by_shape<T, BwdLaunch, true>(slot_shape(c.d, true), a, dim3(uint32_t(a.sp.blocks)), s);
   if (c.w_post || c.gate || g.gH) {
     const uint32_t gates = c.gate && !a.sp.many ? uint32_t(c.gate_rows) : 0;
-    hipLaunchKernelGGL(k_stage_norm_grads, dim3(uint32_t((c.d + 15) / 16), 2 + gates), dim3(256), 0, s, g.ws,
+    hipLaunchKernelGGL(k_stage_norm_grads, dim3(uint32_t((c.d + 31) / 32), 2 + gates), dim3(256), 0, s, g.ws,
                        c.w_post ? g.g_w_post : nullptr, g.gH ? g.g_w_pre : nullptr, gates ? g.g_gate : nullptr,
                        a.sp.blocks, a.sp.bpg, a.d, g.accumulate);
   }
