@@ -244,6 +244,20 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// acc += a b^T of one MFMA tile over 64 columns; see Tile for EXACT
+template <bool EXACT>
+__device__ __forceinline__ f32x16 mac64(i32x8 b, i32x8 a, int eb, int ea, f32x16 acc) {
+  if constexpr (!EXACT) {
+    return mfma_e4m3(b, a, acc, eb, ea);
+  } else {
+    const float sa = __uint_as_float(uint32_t(ea) << 23), sb = __uint_as_float(uint32_t(eb) << 23);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      acc = mfma_bf16_32x32x16(widen8(b[2 * c], b[2 * c + 1], sb), widen8(a[2 * c], a[2 * c + 1], sa), acc);
+    return acc;
+  }
+}
+
 struct GemmArgs {
   View A, B;
   void* C;
@@ -456,6 +470,75 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
   }
 }
 
+// Few rows (M <= 32 FM): the weight's bytes are what counts.  A block has 32
+// columns of C; its 8 waves take every 8th block of 128 columns of the operands,
+// straight from memory into registers (the pack's order is the operand order), and
+// add up through LDS.  One launch, no partial sums in memory.
+constexpr int kFewWaves = 8;
+template <int FM>
+constexpr int kFewLds = kFewWaves * FM * 16 * 65 * 4;  // 64 lanes and one more, against bank conflicts
+
+template <typename T, bool EXACT, int FM>
+__global__ __launch_bounds__(64 * kFewWaves) void k_fp8_few(GemmArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  float* sums = reinterpret_cast<float*>(smem);
+  const int w = wave_id(), l = threadIdx.x & 63;
+  const int64_t tn = blockIdx.x, KB = g.A.KB;
+  struct Operands {
+    u32x4 b[4], a[FM][4];
+    int eb, ea[FM];
+  };
+  const auto load = [&](Operands& o, int64_t kb) {
+    const uint8_t* pb = g.B.code + (tn * KB + kb) * 4096 + l * 16;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) o.b[p] = *reinterpret_cast<const u32x4*>(pb + p * 1024);
+    o.eb = g.B.exp[kb * g.B.exp_stride + tn * 32 + (l & 31)];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t rt = min(int64_t(i), g.A.RT - 1);
+      const uint8_t* pa = g.A.code + (rt * KB + kb) * 4096 + l * 16;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) o.a[i][p] = *reinterpret_cast<const u32x4*>(pa + p * 1024);
+      o.ea[i] = g.A.exp[kb * g.A.exp_stride + rt * 32 + (l & 31)];
+    }
+  };
+  const auto pair = [](u32x4 x, u32x4 y) {
+    return i32x8{int(x[0]), int(x[1]), int(x[2]), int(x[3]), int(y[0]), int(y[1]), int(y[2]), int(y[3])};
+  };
+  f32x16 acc[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
+  Operands cur, nxt;
+  if (w < KB) load(cur, w);
+  for (int64_t kb = w; kb < KB; kb += kFewWaves) {
+    load(nxt, min(kb + kFewWaves, KB - 1));
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[i] = mac64<EXACT>(pair(cur.b[2 * s], cur.b[2 * s + 1]), pair(cur.a[i][2 * s], cur.a[i][2 * s + 1]), cur.eb,
+                              cur.ea[i], acc[i]);
+    cur = nxt;
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) sums[((w * FM + i) * 16 + v) * 65 + l] = acc[i][v];
+  __syncthreads();
+  T* C = static_cast<T*>(g.C);
+  const int n = threadIdx.x & 31, v = 4 * (n >> 3) + (n & 3), hi = (n >> 2) & 1;  // column n: register v, half hi
+  for (int m = threadIdx.x >> 5; m < FM * 32; m += 2 * kFewWaves) {
+    if (m >= g.M || tn * 32 + n >= g.N) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kFewWaves; ++k) s += sums[((k * FM + (m >> 5)) * 16 + v) * 65 + hi * 32 + (m & 31)];
+    T* c = C + m * g.N + tn * 32 + n;
+    *c = from_f32<T>(g.accumulate ? to_f32<T>(*c) + s : s);
+  }
+}
+
 // C (+)= sum of the splits' partial sums, in order; no splits: zeros
 template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_join(const float* part, int splits, T* C, int64_t n, int accumulate) {
@@ -472,10 +555,11 @@ void join_t(const float* part, int splits, T* C, int64_t n, int accumulate, hipS
                      splits, C, n, accumulate);
 }
 
-// How a product is cut: 256 x 256 tiles where they fill the chip, else 128 x 128,
-// with K split into parts of 4 blocks at least while there are fewer tiles than CUs.
+// How a product is cut: up to 128 rows go to k_fp8_few; then 256 x 256 tiles where
+// they fill the chip, else 128 x 128, with K split into parts of 4 blocks at least
+// while there are fewer tiles than CUs.
 struct Cut {
-  bool big;
+  bool few, big;
   int splits;
   int64_t kb_per;
 };
@@ -484,8 +568,9 @@ Cut cut(int64_t M, int64_t N, int64_t K) {
   const int64_t KB = (K + 127) / 128;
   const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   Cut c;
-  c.big = tiles(256) >= kCus;
-  const int64_t want = c.big ? 1 : std::min(kCus / tiles(128), KB / 4);
+  c.few = M <= 128;
+  c.big = !c.few && tiles(256) >= kCus;
+  const int64_t want = c.few || c.big ? 1 : std::min(kCus / tiles(128), KB / 4);
   c.kb_per = want > 1 ? (KB + want - 1) / want : KB;
   c.splits = int((KB + c.kb_per - 1) / c.kb_per);
   return c;
@@ -499,10 +584,23 @@ void gemm_k(const GemmArgs& g, hipStream_t s) {
   hipLaunchKernelGGL(K, dim3(uint32_t(tiles * g.splits)), dim3(TL::kThreads), (LdsLimit<K, TL::kLds>::bytes()), s, g);
 }
 
+template <typename T, bool EXACT, int FM>
+void few_k(const GemmArgs& g, hipStream_t s) {
+  constexpr auto K = k_fp8_few<T, EXACT, FM>;
+  hipLaunchKernelGGL(K, dim3(uint32_t(g.B.RT)), dim3(64 * kFewWaves), (LdsLimit<K, kFewLds<FM>>::bytes()), s, g);
+}
+
 template <typename T>
 void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
   constexpr bool kExact = sizeof(T) == 4;
-  if (c.splits > 1) {
+  if (c.few) {
+    if (g.A.RT == 1)
+      few_k<T, kExact, 1>(g, s);
+    else if (g.A.RT == 2)
+      few_k<T, kExact, 2>(g, s);
+    else
+      few_k<T, kExact, 4>(g, s);
+  } else if (c.splits > 1) {
     T* C = static_cast<T*>(g.C);
     const int accumulate = g.accumulate;
     g.C = ws;

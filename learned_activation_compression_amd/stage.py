@@ -60,13 +60,21 @@ def stage_symbols() -> list:
     return re.findall(r"^\s*(?:int|size_t)\s+([a-z][a-z0-9_]*)\s*\(", text, flags=re.M)
 
 
+# the current stream's handle without a Stream object around it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """Runs a call on the device of its tensors, and allocates on its stream."""
+
+    __slots__ = ("device", "index", "other", "stream", "side", "handle")
 
     def __init__(self, like: torch.Tensor, stream):
         _dev(like, "the first tensor")
         self.device = like.device
-        self.other = torch.cuda.device(like.device) if torch.cuda.current_device() != like.device.index else None
+        self.index = index = self.device.index
+        self.other = torch.cuda.device(index) if torch.cuda.current_device() != index else None
         self.stream = stream
         self.side = torch.cuda.stream(stream) if stream is not None else None
 
@@ -75,7 +83,7 @@ class _On:
             self.other.__enter__()
         if self.side is not None:
             self.side.__enter__()
-        self.handle = (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+        self.handle = _raw_stream(self.index) if self.stream is None else self.stream.cuda_stream
         return self
 
     def __exit__(self, *exc):
@@ -88,10 +96,16 @@ class _On:
         """Device pointer of an optional tensor of this call's device."""
         if t is None:
             return None
-        p = _dev(t, name, dtype)
+        try:
+            if t.get_device() == self.index and t.is_contiguous() and (dtype is None or t.dtype is dtype) and \
+                    (shape is None or t.shape == shape):
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        p = _dev(t, name, dtype)  # names what is wrong
         if t.device != self.device:
             raise MaplError(-1, "binding", f"{name} is on {t.device}, not {self.device}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise MaplError(-2, "binding", f"{name} must be {list(shape)}, got {list(t.shape)}")
         return p
 
@@ -104,6 +118,7 @@ class _On:
             if need == 0:
                 return None, None, 0
             buf = self.empty(need, torch.uint8)
+            return buf, buf.data_ptr(), need
         return buf, self.ptr(buf, name), buf.numel() * buf.element_size()
 
 
@@ -129,7 +144,7 @@ def stage_dropout(X, p, seed, offset=0, Y=None, stream=None) -> torch.Tensor:
     N, d = _rows(X, "X")
     with _On(X, stream) as on:
         if Y is None:
-            Y = on.empty(X.shape, X.dtype)
+            Y = torch.empty_like(X)
         _check(_stage_lib().stage_dropout(on.ptr(X, "X"), on.ptr(Y, "Y", X.dtype, X.shape), float(p),
                                           _u(seed, "seed"), _u(offset, "offset"), N, d, _dt(X), on.handle),
                "stage_dropout")
@@ -146,9 +161,9 @@ def stage_norm(X, Y=None, w_post=None, gate=None, w_pre=None, res_scale=1.0, eps
     dt = X.dtype
     with _On(X, stream) as on:
         if X_out is None and store_x:
-            X_out = on.empty(X.shape, dt)
+            X_out = torch.empty_like(X)
         if H is None and w_pre is not None:
-            H = on.empty(X.shape, dt)
+            H = torch.empty_like(X)
         G = 0 if gate is None else gate.shape[0]
         _check(_stage_lib().stage_norm(on.ptr(X, "X"), on.ptr(Y, "Y", dt, X.shape), on.ptr(w_post, "w_post", dt, (d,)),
                                        on.ptr(gate, "gate", dt, (G, d)), on.ptr(w_pre, "w_pre", dt, (d,)),
@@ -182,8 +197,8 @@ def stage_norm_bwd(gX_out=None, gH=None, X_out=None, Y=None, w_post=None, gate=N
             return torch.zeros(size, dtype=torch.float32, device=on.device) if accumulate else \
                 on.empty(size, torch.float32)
 
-        gX = on.empty(shape, dt) if gX is None else gX
-        gY = None if Y is None else on.empty(shape, dt) if gY is None else gY
+        gX = torch.empty_like(like) if gX is None else gX
+        gY = None if Y is None else torch.empty_like(like) if gY is None else gY
         g_w_post = grad(g_w_post, w_post is not None, (d,))
         g_gate = grad(g_gate, gate is not None, (G, d))
         g_w_pre = grad(g_w_pre, gH is not None, (d,))
