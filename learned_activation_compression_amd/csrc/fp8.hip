@@ -280,14 +280,14 @@ struct GemmArgs {
 //  - fp32 (weight gradients): the codes times their scales are widened to bf16,
 //    which holds them exactly, and go through the bf16 instruction, whose sums
 //    are fp32 throughout (1e-8 on the same data).
-template <int WM, int WN, int FM, int FN>
+template <int WM, int WN, int FM, int FN, int NS>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kBM = WM * FM, kBN = WN * FN;  // units of 32 rows
   static constexpr int kUnits = kBM + kBN;
   static constexpr int kStage = kUnits * 4096 + 512;   // codes, then 256 + 256 bytes of exponents
   static constexpr int kPieces = kUnits * 4 / kWaves;  // 1 KB pieces each wave copies per stage
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLds = NS * kStage;
   static_assert(kUnits * 4 % kWaves == 0 && kPieces % 4 == 0 && kPieces % FM == 0 && kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
 };
 
@@ -308,12 +308,12 @@ __device__ __forceinline__ void put16(float* c, const char* src, int left, int a
     st_tail4(c, __builtin_bit_cast(u32x4, v), left);
 }
 
-// The loop runs one stage (128 columns) ahead in LDS and one step (64 columns)
-// ahead in registers, with one barrier a stage: behind it the stage just read is
-// free for the copy of the stage after next, and the next one is complete.
-template <typename T, bool EXACT, int WM, int WN, int FM, int FN>
+// The loop runs NS - 1 stages (of 128 columns) ahead in LDS and one step (64
+// columns) ahead in registers, with one barrier a stage: behind it the stage just
+// read is free for the copy of the stage NS later, and the next one is complete.
+template <typename T, bool EXACT, int WM, int WN, int FM, int FN, int NS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
-  using TL = Tile<WM, WN, FM, FN>;
+  using TL = Tile<WM, WN, FM, FN, NS>;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int w = wave_id(), l = threadIdx.x & 63, wm = w / WN, wn = w % WN;
   const uint32_t tiles_m = static_cast<uint32_t>((g.A.RT + TL::kBM - 1) / TL::kBM);
@@ -338,9 +338,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(smem)));
   const uint8_t* exps = (w & 1) ? g.B.exp + tn * 32 : g.A.exp + tm * 32;
   const int64_t exp_stride = (w & 1) ? g.B.exp_stride : g.A.exp_stride;
+  const auto slot = [](int64_t kb) { return static_cast<uint32_t>(kb) % NS; };
   // part i of FM of the copies of a stage
   auto fetch = [&](int64_t kb, int i) {
-    const uint32_t st = lds0 + static_cast<uint32_t>(kb & 1) * TL::kStage;
+    const uint32_t st = lds0 + slot(kb) * TL::kStage;
 #pragma unroll
     for (int p = i * (TL::kPieces / FM); p < (i + 1) * (TL::kPieces / FM); ++p)
       copy_lane16_to_lds(src[p >> 2] + kb * 4096 + (p & 3) * 1024, l * 16, st + (w * TL::kPieces + p) * 1024);
@@ -363,7 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
   Step s0, s1;
   // part i of FM of the operands of step s of stage kb; the column operand first, every row needs it
   auto read = [&](Step& st, int64_t kb, int s, int i) {
-    const char* at = smem + (kb & 1) * TL::kStage + s * 2048 + l * 16;
+    const char* at = smem + slot(kb) * TL::kStage + s * 2048 + l * 16;
 #pragma unroll
     for (int f = i * (FM + FN) / FM; f < (i + 1) * (FM + FN) / FM; ++f) {
       if (f < FN)
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
     }
   };
   auto read_exp = [&](Step& st, int64_t kb) {
-    const char* ex = smem + (kb & 1) * TL::kStage + TL::kUnits * 4096 + (l & 31);
+    const char* ex = smem + slot(kb) * TL::kStage + TL::kUnits * 4096 + (l & 31);
 #pragma unroll
     for (int i = 0; i < FM; ++i) st.ea[i] = static_cast<uint8_t>(ex[(wm * FM + i) * 32]);
 #pragma unroll
@@ -396,20 +397,21 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
     }
   };
 
+  for (int64_t kb = k0; kb < min(k0 + NS, k1); ++kb)
 #pragma unroll
-  for (int i = 0; i < FM; ++i) fetch(k0, i);
-  wait_vmcnt<0>();
+    for (int i = 0; i < FM; ++i) fetch(kb, i);
+  if (k0 + NS <= k1)
+    wait_vmcnt<(NS - 1) * (TL::kPieces + 1)>();  // the first stage: the others may be on their way
+  else
+    wait_vmcnt<0>();
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    if (k0 + 1 < k1) fetch(k0 + 1, i);
-    read(s0, k0, 0, i);
-  }
   read_exp(s0, k0);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) read(s0, k0, 0, i);
   // One stage.  sched_barrier: each part's reads and copies are issued beside its
   // MFMAs, not in one run ahead of them.  A branch in here would let the compiler
-  // sink the MFMAs below it, so the last two stages are bodies of their own.
-  auto stage = [&](int64_t kb, auto next, auto next2) {
+  // sink the MFMAs below it, so the last NS stages are bodies of their own.
+  auto stage = [&](int64_t kb, auto next, auto copy) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       read(s1, kb, 1, i);
@@ -421,21 +423,22 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
 #pragma unroll
     for (int i = 0; i < FN; ++i) s1.eb[i] = s0.eb[i];
     if constexpr (next) {
-      wait_vmcnt<0>();
+      // stage kb + 1 is there when only the NS - 2 behind it are outstanding; none is issued any more near the end
+      wait_vmcnt<copy ? (NS - 2) * (TL::kPieces + 1) : 0>();
       __syncthreads();
       read_exp(s0, kb + 1);
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      if constexpr (next2) fetch(kb + 2, i);
+      if constexpr (copy) fetch(kb + NS, i);
       if constexpr (next) read(s0, kb + 1, 0, i);
       multiply(s1, i);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   int64_t kb = k0;
-  for (; kb + 2 < k1; ++kb) stage(kb, std::true_type{}, std::true_type{});
-  if (kb + 1 < k1) stage(kb++, std::true_type{}, std::false_type{});
+  for (; kb + NS < k1; ++kb) stage(kb, std::true_type{}, std::true_type{});
+  for (; kb + 1 < k1; ++kb) stage(kb, std::true_type{}, std::false_type{});
   stage(kb, std::false_type{}, std::false_type{});
 
   // acc[i][k]: row (tm + wm FM + i) * 32 + (l & 31) of C, columns (tn + wn FN + k) * 32 + mfma32_row(v, l >> 5).
@@ -539,27 +542,40 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_fp8_few(GemmArgs g) {
   }
 }
 
-// C (+)= sum of the splits' partial sums, in order; no splits: zeros
+// C (+)= sum of the splits' partial sums, in order; no splits: zeros.  A thread
+// has 4 neighbouring elements of the whole.
 template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_join(const float* part, int splits, T* C, int64_t n, int accumulate) {
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-    float s = 0.f;
-    for (int k = 0; k < splits; ++k) s += part[k * n + i];
-    C[i] = from_f32<T>(accumulate ? to_f32<T>(C[i]) + s : s);
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < n; i += int64_t(gridDim.x) * 1024) {
+    const int left = static_cast<int>(min(n - i, int64_t(4)));
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k)
+      s += __builtin_bit_cast(f32x4, left == 4 ? ld16B(part + k * n + i) : ld_tail4(part + k * n + i, left));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) C[i + e] = from_f32<T>(accumulate ? to_f32<T>(C[i + e]) + s[e] : s[e]);
   }
 }
 
 template <typename T>
 void join_t(const float* part, int splits, T* C, int64_t n, int accumulate, hipStream_t s) {
-  hipLaunchKernelGGL(k_fp8_join<T>, dim3(uint32_t(std::min<int64_t>((n + 255) / 256, 4096))), dim3(256), 0, s, part,
+  hipLaunchKernelGGL(k_fp8_join<T>, dim3(uint32_t(std::min<int64_t>((n + 1023) / 1024, 2048))), dim3(256), 0, s, part,
                      splits, C, n, accumulate);
 }
 
-// How a product is cut: up to 128 rows go to k_fp8_few; then 256 x 256 tiles where
-// they fill the chip, else 128 x 128, with K split into parts of 4 blocks at least
-// while there are fewer tiles than CUs.
+// How a product is cut (times: one MI355X, bf16 C unless stated):
+//  - few rows, M <= 128: k_fp8_few (128 x 2048 x 2048: 6.4 us, 64 x 64 tiles 6.7, 128 x 128 tiles 10);
+//  - 256 x 256 tiles where they fill the 256 CUs (4000 x 4096 x 4096: 52 us, 128 x 128 tiles 62);
+//  - 128 x 128 tiles from 160 of them (2000 x 2048 x 2048, 256 tiles: 12.4 us, 64 x 64 tiles 16): with two
+//    workgroups a CU and 2 stages each, or with one and 4 (2048 x 2048 x 8192: 35 us, with 2 stages 43);
+//  - fewer: 64 x 64 tiles (1000 x 2048 x 2048: 9.5 us, 128 x 128 tiles 11.0), or, where parts of 32 blocks of K
+//    are left for it, 128 x 128 tiles with K split (1024 x 1024 x 16384 fp32: 38 against 52 us): partial sums in
+//    memory and a second launch cost 10 us, which shorter parts do not pay for.
+enum CutKind { kFew, kTile64, kTile128, kTile256 };
 struct Cut {
-  bool few, big;
+  CutKind kind;
+  bool deep;  // 128 x 128 tiles: one workgroup a CU
   int splits;
   int64_t kb_per;
 };
@@ -567,19 +583,29 @@ Cut cut(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kCus = 256;
   const int64_t KB = (K + 127) / 128;
   const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
-  Cut c;
-  c.few = M <= 128;
-  c.big = !c.few && tiles(256) >= kCus;
-  const int64_t want = c.few || c.big ? 1 : std::min(kCus / tiles(128), KB / 4);
-  c.kb_per = want > 1 ? (KB + want - 1) / want : KB;
-  c.splits = int((KB + c.kb_per - 1) / c.kb_per);
+  const int64_t t128 = tiles(128), parts = std::min(kCus / t128, KB / 32);
+  Cut c{kFew, false, 1, KB};
+  if (M <= 128) return c;
+  if (tiles(256) >= kCus) {
+    c.kind = kTile256;
+  } else if (t128 >= 160) {
+    c.kind = kTile128;
+    c.deep = t128 <= kCus;
+  } else if (parts >= 2) {
+    c.kind = kTile128;
+    c.deep = true;
+    c.kb_per = (KB + parts - 1) / parts;
+    c.splits = int((KB + c.kb_per - 1) / c.kb_per);
+  } else {
+    c.kind = kTile64;
+  }
   return c;
 }
 
-template <typename T, bool EXACT, int WM, int WN, int FM, int FN>
+template <typename T, bool EXACT, int WM, int WN, int FM, int FN, int NS>
 void gemm_k(const GemmArgs& g, hipStream_t s) {
-  using TL = Tile<WM, WN, FM, FN>;
-  constexpr auto K = k_fp8_gemm<T, EXACT, WM, WN, FM, FN>;
+  using TL = Tile<WM, WN, FM, FN, NS>;
+  constexpr auto K = k_fp8_gemm<T, EXACT, WM, WN, FM, FN, NS>;
   const int64_t tiles = (g.A.RT + TL::kBM - 1) / TL::kBM * ((g.B.RT + TL::kBN - 1) / TL::kBN);
   hipLaunchKernelGGL(K, dim3(uint32_t(tiles * g.splits)), dim3(TL::kThreads), (LdsLimit<K, TL::kLds>::bytes()), s, g);
 }
@@ -593,7 +619,7 @@ void few_k(const GemmArgs& g, hipStream_t s) {
 template <typename T>
 void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
   constexpr bool kExact = sizeof(T) == 4;
-  if (c.few) {
+  if (c.kind == kFew) {
     if (g.A.RT == 1)
       few_k<T, kExact, 1>(g, s);
     else if (g.A.RT == 2)
@@ -605,12 +631,16 @@ void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
     const int accumulate = g.accumulate;
     g.C = ws;
     g.accumulate = 0;
-    gemm_k<float, kExact, 2, 2, 2, 2>(g, s);
+    gemm_k<float, kExact, 2, 2, 2, 2, 4>(g, s);
     join_t(ws, c.splits, C, g.M * g.N, accumulate, s);
-  } else if (c.big) {
-    gemm_k<T, kExact, 2, 4, 4, 2>(g, s);
+  } else if (c.kind == kTile256) {
+    gemm_k<T, kExact, 2, 4, 4, 2, 2>(g, s);
+  } else if (c.kind == kTile64) {
+    gemm_k<T, kExact, 2, 2, 1, 1, 4>(g, s);
+  } else if (c.deep) {
+    gemm_k<T, kExact, 2, 2, 2, 2, 4>(g, s);
   } else {
-    gemm_k<T, kExact, 2, 2, 2, 2>(g, s);
+    gemm_k<T, kExact, 2, 2, 2, 2, 2>(g, s);
   }
 }
 
