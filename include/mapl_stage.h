@@ -117,7 +117,7 @@ int stage_norm_bwd(const void* gX_out, const void* gH, const void* X_out, const 
  * X): forward Y = X W^T takes (X, W), gX = gY W takes (gY, W^T) and gW = gY^T X
  * takes (gY^T, X^T).  Either may be NULL, not both.  Packs are 16-byte aligned
  * (MAPL_ERR_ARG) and at least fp8_pack_bytes() of their own rows and columns
- * (MAPL_ERR_WORKSPACE).  0 <= R, C <= 2^30, R C <= 2^36
+ * (MAPL_ERR_WORKSPACE).  0 <= R, C <= 2^27, R C <= 2^36
  * (MAPL_ERR_SHAPE).
  * ---------------------------------------------------------------------- */
 size_t fp8_pack_bytes(int64_t rows, int64_t cols);

@@ -569,13 +569,14 @@ void join_t(const float* part, int splits, T* C, int64_t n, int accumulate, hipS
 //  - 256 x 256 tiles where they fill the 256 CUs (4000 x 4096 x 4096: 52 us, 128 x 128 tiles 62);
 //  - 128 x 128 tiles from 160 of them (2000 x 2048 x 2048, 256 tiles: 12.4 us, 64 x 64 tiles 16): with two
 //    workgroups a CU and 2 stages each, or with one and 4 (2048 x 2048 x 8192: 35 us, with 2 stages 43);
-//  - fewer: 64 x 64 tiles (1000 x 2048 x 2048: 9.5 us, 128 x 128 tiles 11.0), or, where parts of 32 blocks of K
-//    are left for it, 128 x 128 tiles with K split (1024 x 1024 x 16384 fp32: 38 against 52 us): partial sums in
-//    memory and a second launch cost 10 us, which shorter parts do not pay for.
+//  - fewer: 64 x 64 tiles (1000 x 2048 x 2048: 9.5 us, 128 x 128 tiles 11.0), or, for K of 8192 and more,
+//    128 x 128 tiles with K split into parts of 2048 at least, one or two workgroups a CU (1024 x 1024 x 8192 fp32:
+//    28 us, 64 x 64 tiles 34).  Partial sums in memory and a second launch cost 5 to 10 us, which a shorter K does
+//    not pay for (1000 x 1024 x 4096: 16.5 us, 64 x 64 tiles 10.6).
 enum CutKind { kFew, kTile64, kTile128, kTile256 };
 struct Cut {
   CutKind kind;
-  bool deep;  // 128 x 128 tiles: one workgroup a CU
+  bool deep;  // 128 x 128 tiles: at most one workgroup a CU
   int splits;
   int64_t kb_per;
 };
@@ -583,7 +584,7 @@ Cut cut(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kCus = 256;
   const int64_t KB = (K + 127) / 128;
   const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
-  const int64_t t128 = tiles(128), parts = std::min(kCus / t128, KB / 32);
+  const int64_t t128 = tiles(128), parts = std::min((2 * t128 <= kCus ? 1 : 2) * kCus / t128, KB / 16);
   Cut c{kFew, false, 1, KB};
   if (M <= 128) return c;
   if (tiles(256) >= kCus) {
@@ -591,11 +592,11 @@ Cut cut(int64_t M, int64_t N, int64_t K) {
   } else if (t128 >= 160) {
     c.kind = kTile128;
     c.deep = t128 <= kCus;
-  } else if (parts >= 2) {
+  } else if (KB >= 64 && parts >= 2) {
     c.kind = kTile128;
-    c.deep = true;
     c.kb_per = (KB + parts - 1) / parts;
     c.splits = int((KB + c.kb_per - 1) / c.kb_per);
+    c.deep = t128 * c.splits <= kCus;
   } else {
     c.kind = kTile64;
   }
@@ -631,7 +632,10 @@ void gemm_t(GemmArgs g, const Cut& c, float* ws, hipStream_t s) {
     const int accumulate = g.accumulate;
     g.C = ws;
     g.accumulate = 0;
-    gemm_k<float, kExact, 2, 2, 2, 2, 4>(g, s);
+    if (c.deep)
+      gemm_k<float, kExact, 2, 2, 2, 2, 4>(g, s);
+    else
+      gemm_k<float, kExact, 2, 2, 2, 2, 2>(g, s);
     join_t(ws, c.splits, C, g.M * g.N, accumulate, s);
   } else if (c.kind == kTile256) {
     gemm_k<T, kExact, 2, 4, 4, 2, 2>(g, s);

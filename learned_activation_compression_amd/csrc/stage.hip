@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void k_dropout(const T* X, T* Y, Drop dr, int6
     x[k].issue(X + (u0 + k * 256 < units ? row[k] : 0) * d, int64_t(b[k]) * 8, d);
   }
 #pragma unroll
-  for (int k = 0; k < kDropUnits; ++k) keep[k] = keep8(dr, b[k], static_cast<uint64_t>(row[k]));
+  for (int k = 0; k < kDropUnits; ++k) keep[k] = dr.t ? keep8(dr, b[k], static_cast<uint64_t>(row[k])) : 0xffu;
 #pragma unroll
   for (int k = 0; k < kDropUnits; ++k) {
     const bool in = u0 + k * 256 < units;

@@ -34,7 +34,7 @@ int check_norm_scalars(float res_scale, float eps, double p) {
 }
 
 int check_fp8_shape(int64_t a, int64_t b) {
-  constexpr int64_t top = int64_t(1) << 30;
+  constexpr int64_t top = int64_t(1) << 27;  // a grid has fewer than 2^32 threads
   if (a < 0 || b < 0 || a > top || b > top || (b > 0 && a > kMaxElems / b)) return MAPL_ERR_SHAPE;
   return MAPL_OK;
 }
