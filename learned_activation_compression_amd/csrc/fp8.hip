@@ -53,25 +53,48 @@ __device__ __forceinline__ float finite_abs(float x) {
   return b < 0x7f800000u ? __uint_as_float(b) : 0.f;
 }
 
+// Largest finite magnitude of n values; `bad`: some are not finite.  As integers
+// the magnitudes compare as they do as floats, with those beyond infinity on top, so
+// the values are looked at one by one only where there is one.
+template <int N>
+__device__ __forceinline__ float abs_max(const float* v, bool& bad) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  bad = m >= 0x7f800000u;
+  float f = __uint_as_float(m);
+  if (bad) {
+    f = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f = fmaxf(f, finite_abs(v[i]));
+  }
+  return f;
+}
+
 // 4 values times 2^-s to e4m3 codes; the scaled values are at most 448 in size
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
   int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
   r = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, r, true);
-  uint32_t c = static_cast<uint32_t>(r);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if ((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u) c |= 0x7fu << (8 * i);
-  return c;
+  return static_cast<uint32_t>(r);
 }
-__device__ __forceinline__ u32x4 codes16(const float* v, float inv) {
-  return u32x4{codes4(v, inv), codes4(v + 4, inv), codes4(v + 8, inv), codes4(v + 12, inv)};
+// 16 of them; `bad` (abs_max): those that are not finite become NaN
+__device__ __forceinline__ u32x4 codes16(const float* v, float inv, bool bad) {
+  u32x4 c = {codes4(v, inv), codes4(v + 4, inv), codes4(v + 8, inv), codes4(v + 12, inv)};
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u) c[i >> 2] |= 0x7fu << (8 * (i & 3));
+  }
+  return c;
 }
 
 // ---------------------------------------------------------------------- pack --
 // A block takes 128 rows x 128 columns of X.  Thread (i, j) = (tid / 8, tid % 8)
 // holds rows i + 32 k (k = 0..3), columns 16 j .. 16 j + 15.  The row operand
 // needs the sizes of 8 neighbouring lanes only.  The column operand goes through
-// LDS: wave w then holds rows 32 w .. 32 w + 31 of two columns per lane.
+// LDS: wave w then holds rows 32 w .. 32 w + 31 of two columns per lane.  16384 x
+// 1024 bf16 out of memory: the column operand 13.8 us (3.6 TB/s), both 17.0 (3.9);
+// with every value tested for infinity and NaN (abs_max) 15.7 and 19.7.
 template <typename T, RowMode MODE, bool ROWS, bool COLS>
 __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, int square, int64_t R, int64_t C) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -82,6 +105,7 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
   const int64_t kb = blockIdx.x % nkb, rb = blockIdx.x / nkb;
   const int64_t c = kb * 128 + 16 * j;
   float v[4][16], am[4];
+  bool bad[4];
   Fetch<T, MODE> f[4][2];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -98,9 +122,7 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
       v[k][i] = lo.get(i);
       v[k][8 + i] = hi.get(i);
     }
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[k][i]));
+    float m = abs_max<16>(v[k], bad[k]);
     m = fmaxf(m, __shfl_xor(m, 1));
     m = fmaxf(m, __shfl_xor(m, 2));
     am[k] = fmaxf(m, __shfl_xor(m, 4));
@@ -120,7 +142,7 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
       const int64_t rt = rb * 4 + k;
       if (rt < pr.RT) {
         const int e = block_exp(am[k]);
-        *reinterpret_cast<u32x4*>(pr.code + (rt * pr.KB + kb) * 4096 + unit_off(i0, j)) = codes16(v[k], pow2_neg(e));
+        *reinterpret_cast<u32x4*>(pr.code + (rt * pr.KB + kb) * 4096 + unit_off(i0, j)) = codes16(v[k], pow2_neg(e), bad[k]);
         if (j == 0) pr.exp[kb * pr.exp_stride + rt * 32 + i0] = static_cast<uint8_t>(e);
       }
     }
@@ -139,7 +161,6 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
       }
     __syncthreads();
     const int w = tid >> 6, l = tid & 63;
-    float m0 = 0.f, m1 = 0.f;
     float a0[32], a1[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -153,9 +174,9 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
         a0[i] = __uint_as_float(u[0]);
         a1[i] = __uint_as_float(u[1]);
       }
-      m0 = fmaxf(m0, finite_abs(a0[i]));
-      m1 = fmaxf(m1, finite_abs(a1[i]));
     }
+    bool bad0, bad1;
+    float m0 = abs_max<32>(a0, bad0), m1 = abs_max<32>(a1, bad1);
     if (square) {
       m0 = m1 = am[0];
     } else {
@@ -177,8 +198,8 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
       const int r = (2 * l) & 31;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<u32x4*>(base + unit_off(r, 2 * w + h)) = codes16(a0 + 16 * h, pow2_neg(e0));
-        *reinterpret_cast<u32x4*>(base + unit_off(r + 1, 2 * w + h)) = codes16(a1 + 16 * h, pow2_neg(e1));
+        *reinterpret_cast<u32x4*>(base + unit_off(r, 2 * w + h)) = codes16(a0 + 16 * h, pow2_neg(e0), bad0);
+        *reinterpret_cast<u32x4*>(base + unit_off(r + 1, 2 * w + h)) = codes16(a1 + 16 * h, pow2_neg(e1), bad1);
       }
       if (w == 0) {
         uint8_t* ex = pc.exp + rb * pc.exp_stride + rt * 32 + r;
@@ -191,7 +212,7 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const T* X, View pr, View pc, 
 
 // The row operand alone, scaled by rows: 32 rows x 512 columns a block, so that a
 // row is read 1 KB at a time and the codes leave as 16 KB in one piece (32768 x 2048
-// bf16 out of memory: 40 us, 5.0 TB/s; by 128 x 128 tiles 44 us).
+// bf16 out of memory: 39 us, 5.2 TB/s; by 128 x 128 tiles 4 us more).
 template <typename T, RowMode MODE>
 __global__ __launch_bounds__(256) void k_fp8_pack_rows(const T* X, View p, int64_t R, int64_t C) {
   const int i0 = threadIdx.x >> 3, j = threadIdx.x & 7;
@@ -209,20 +230,20 @@ __global__ __launch_bounds__(256) void k_fp8_pack_rows(const T* X, View p, int64
   for (int k = 0; k < 4; ++k) {
     const int64_t kb = kb0 + k, c = kb * 128 + 16 * j;
     const Raw8<T> lo = f[k][0].value(c, C, in), hi = f[k][1].value(c + 8, C, in);
-    float v[16], m = 0.f;
+    float v[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = lo.get(i);
       v[8 + i] = hi.get(i);
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[i]));
+    bool bad;
+    float m = abs_max<16>(v, bad);
     m = fmaxf(m, __shfl_xor(m, 1));
     m = fmaxf(m, __shfl_xor(m, 2));
     m = fmaxf(m, __shfl_xor(m, 4));
     if (kb < p.KB) {
       const int e = block_exp(m);
-      *reinterpret_cast<u32x4*>(p.code + (rt * p.KB + kb) * 4096 + unit_off(i0, j)) = codes16(v, pow2_neg(e));
+      *reinterpret_cast<u32x4*>(p.code + (rt * p.KB + kb) * 4096 + unit_off(i0, j)) = codes16(v, pow2_neg(e), bad);
       if (j == 0) p.exp[kb * p.exp_stride + rt * 32 + i0] = static_cast<uint8_t>(e);
     }
   }
@@ -350,6 +371,12 @@ __device__ __forceinline__ void put16(float* c, const char* src, int left, int a
 // The loop runs NS - 1 stages (of 128 columns) ahead in LDS and one step (64
 // columns) ahead in registers, with one barrier a stage: behind it the stage just
 // read is free for the copy of the stage NS later, and the next one is complete.
+// 8192 x 8192 x 8192: 389 us, 2830 TFLOP/s, where MFMAs alone on zeros reach 5000.
+// Without the copies (the same operands over and over) 4096 x 4096 x 8192 takes 90
+// instead of 101 us, without the reads from LDS 99: the matrix cores are the bound,
+// at the clock that random data leaves them.  32768 x 8192 x 2048 takes 530 us, as its 512 MB of C leave in
+// bursts; 128 x 256 tiles, two workgroups a CU, spread them and gain nothing (565 us).
+// Widened operands (EXACT): 8192 x 8192 x 4096 in 400 us, 1370 TFLOP/s.
 template <typename T, bool EXACT, int WM, int WN, int FM, int FN, int NS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
   using TL = Tile<WM, WN, FM, FN, NS>;

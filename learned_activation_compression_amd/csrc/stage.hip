@@ -58,7 +58,10 @@ Drop make_drop(double p, uint64_t seed, uint64_t offset) {
 }
 
 // ------------------------------------------------------------------- dropout --
-// Units of 8 columns, unit u = row * nb + column / 8.
+// Units of 8 columns, unit u = row * nb + column / 8: one generator call each, 20
+// products of 32 by 32 bits for 16 bits an element, which hides behind the traffic:
+// 16384 x 1024 bf16 out of memory in 12.2 us, 5.5 TB/s, as a copy (a fifth more with
+// two calls, 32 bits an element).
 constexpr int kDropUnits = 4;  // units in flight per thread
 
 template <typename T, RowMode MODE>
@@ -159,6 +162,10 @@ struct NormArgs {
   int d;
 };
 
+// Bound by its traffic, two tensors in and two out: 16384 x 1024 bf16 out of memory
+// in 25.8 us (5.2 TB/s) without and 28 us (4.8 TB/s) with dropout, whose generator
+// does not quite hide; 8192 x 2048 in 28.4 us.  All loads of a row, weights included,
+// are issued before the first sum; the weights come from the caches.
 template <typename T, int TPR, int V, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
@@ -285,8 +292,14 @@ struct NormBwdArgs {
   int d, accumulate;
 };
 
-// PRE: with gH and X_out; POST: with Y; MANY: many gate rows.  The loads of the
-// next row are in flight over the arithmetic of this one.
+// PRE: with gH and X_out; POST: with Y; MANY: many gate rows.
+//
+// Four tensors in, two out, and the three weights' sums in registers.  One row is
+// four dependent steps (load, sums, gX and the dot product of gY, gY), so the loads
+// of the next row are issued before this row's arithmetic: 16384 x 1024 bf16 in 39.8
+// us (5.1 TB/s), against 84 us with each row loaded when its turn comes.  512 blocks
+// are what the registers (135 a thread) keep resident; more would only add partial
+// rows to join (4.2 us for 512).
 template <typename T, int TPR, int V, bool PRE, bool POST, bool MANY, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
