@@ -8,7 +8,7 @@
 //    lane l holds row l & 31, columns 64 s + 32 (l >> 5) + 16 h + 0..15.  Every
 //    operand load of a wave is one contiguous kilobyte, from memory or LDS.
 //  - exponents, one byte each, [KB][rows rounded up to 256], then 256 bytes of
-//    slack, so that 256 bytes from any multiple of 128 rows can be read.
+//    slack, so that 256 bytes from the first row of any tile can be read.
 // Codes of padding rows are zero or stale: they only reach output rows that are
 // not stored.  Padding columns are zero in every pack.
 #include <type_traits>

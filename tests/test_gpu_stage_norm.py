@@ -274,3 +274,15 @@ def test_edge_in_a_graph():
         assert torch.equal(xo, ex) and torch.equal(ho, eh) and torch.equal(dr, lac.stage_dropout(gx, 0.1, 9))
         for s, t in zip(out, want):
             assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_everything_dropped(dt):
+    a, rng = edge_inputs(19, 333, dt, True, True, 1)
+    a["Y"].fill_(float("nan"))
+    x, h = lac.stage_norm(**a, p=1.0, seed=4)
+    near(x, n64(a["X"]), np.abs(n64(a["X"])), DT[dt], 4, "X_out")
+    assert h.isfinite().all()
+    gx = rows(rng, 19, 333, dt)
+    g = lac.stage_norm_bwd(gx, None, None, a["Y"], a["w_post"], a["gate"], None, p=1.0, seed=4)
+    assert torch.equal(g[0], gx) and not g[1].any() and not g[2].any() and not g[3].any()
