@@ -348,7 +348,8 @@ struct Tile {
   static constexpr int kStage = kUnits * 4096 + 512;   // codes, then 256 + 256 bytes of exponents
   static constexpr int kPieces = kUnits * 4 / kWaves;  // 1 KB pieces each wave copies per stage
   static constexpr int kLds = NS * kStage;
-  static_assert(kUnits * 4 % kWaves == 0 && kPieces % 4 == 0 && kPieces % FM == 0 && kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
+  static_assert(kUnits * 4 % kWaves == 0 && kPieces % 4 == 0 && kPieces % FM == 0, "every wave copies whole units");
+  static_assert(kLds <= kMaxLdsBytes && kBM <= 8 && kBN <= 8, "tile");
 };
 
 // One row of a wave's output block from LDS to C: 16 bytes per lane.
@@ -374,9 +375,10 @@ __device__ __forceinline__ void put16(float* c, const char* src, int left, int a
 // 8192 x 8192 x 8192: 389 us, 2830 TFLOP/s, where MFMAs alone on zeros reach 5000.
 // Without the copies (the same operands over and over) 4096 x 4096 x 8192 takes 90
 // instead of 101 us, without the reads from LDS 99: the matrix cores are the bound,
-// at the clock that random data leaves them.  32768 x 8192 x 2048 takes 530 us, as its 512 MB of C leave in
-// bursts; 128 x 256 tiles, two workgroups a CU, spread them and gain nothing (565 us).
-// Widened operands (EXACT): 8192 x 8192 x 4096 in 400 us, 1370 TFLOP/s.
+// at the clock that random data leaves them.  32768 x 8192 x 2048 takes 530 us, as
+// its 512 MB of C leave in bursts; 128 x 256 tiles, two workgroups a CU, spread them
+// and gain nothing (565 us).  Widened operands (EXACT): 8192 x 8192 x 4096 in 400 us,
+// 1370 TFLOP/s.
 template <typename T, bool EXACT, int WM, int WN, int FM, int FN, int NS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_fp8_gemm(GemmArgs g) {
   using TL = Tile<WM, WN, FM, FN, NS>;
