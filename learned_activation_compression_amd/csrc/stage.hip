@@ -152,6 +152,13 @@ __device__ __forceinline__ void slot_sums(float (&v)[K], float* lds, int& turn) 
   }
 }
 
+// 1 / sqrt(x) from the hardware's estimate (one unit in the last place) and one
+// Newton step, once a row: the estimate's error would be common to the whole row.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return x < 3.0e38f ? fmaf(0.5f * r, fmaf(-(x * r), r, 1.f), r) : r;
+}
+
 template <typename T>
 struct NormArgs {
   const T *X, *Y, *w_post, *gate, *w_pre;
@@ -222,7 +229,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
       }
       if (a.w_post) {
         slot_sums<TPR>(s, lds, turn);
-        const float q = rsqrtf(s[0] * a.inv_d + a.eps);
+        const float q = inv_sqrt(s[0] * a.inv_d + a.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const Raw8<T> w = fq[j].value(col(j), a.d, true);
@@ -255,7 +262,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[0] += col(j) + i < a.d ? x[j][i] * x[j][i] : 0.f;
       slot_sums<TPR>(s, lds, turn);
-      const float r = rsqrtf(s[0] * a.inv_d + a.eps);
+      const float r = inv_sqrt(s[0] * a.inv_d + a.eps);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const Raw8<T> w = fw[j].value(col(j), a.d, true);
@@ -398,8 +405,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a
       }
     }
     slot_sums<TPR>(s, lds, turn);
-    const float r = rsqrtf(s[0] * a.inv_d + a.eps), m = s[1] * a.inv_d * r * r;
-    const float q = norm ? rsqrtf(s[2] * a.inv_d + a.eps) : 1.f;
+    const float r = inv_sqrt(s[0] * a.inv_d + a.eps), m = s[1] * a.inv_d * r * r;
+    const float q = norm ? inv_sqrt(s[2] * a.inv_d + a.eps) : 1.f;
     float sb[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -489,19 +496,19 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a
 }
 
 // Joins the partial rows: block (x, y) sums 32 columns of one output row, 4
-// columns by 32 runs of rows a thread, in a fixed order.  y = 0: w_post; 1:
-// w_pre; 2 + g: gate row g.
+// columns by 32 runs of rows a thread, in a fixed order, in fp64: it costs nothing
+// here.  y = 0: w_post; 1: w_pre; 2 + g: gate row g.
 __global__ __launch_bounds__(256) void k_stage_norm_grads(const float* part, float* g_w_post, float* g_w_pre,
                                                           float* g_gate, int64_t blocks, int64_t bpg, int d,
                                                           int accumulate) {
-  __shared__ float lds[32][33];
+  __shared__ double lds[32][33];
   const int64_t y = int64_t(blockIdx.y);
   float* out = y == 0 ? g_w_post : y == 1 ? g_w_pre : g_gate ? g_gate + (y - 2) * d : nullptr;
   if (out == nullptr) return;
   const float* src = part + (y == 0 ? 0 : y == 1 ? 2 * blocks : blocks + (y - 2) * bpg) * d;
   const int64_t rows = y < 2 ? blocks : bpg;
   const int cx = (threadIdx.x & 7) * 4, ry = threadIdx.x >> 3, c = blockIdx.x * 32 + cx;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  double s[4] = {0., 0., 0., 0.};
   if (c + 4 <= d) {
 #pragma unroll 8
     for (int64_t r = ry; r < rows; r += 32) {
@@ -520,11 +527,11 @@ __global__ __launch_bounds__(256) void k_stage_norm_grads(const float* part, flo
   __syncthreads();
   const int e = threadIdx.x;
   if (e < 32 && blockIdx.x * 32 + e < static_cast<uint32_t>(d)) {
-    float v = 0.f;
+    double v = 0.;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v += lds[k][e];
     out += blockIdx.x * 32 + e;
-    *out = accumulate ? *out + v : v;
+    *out = accumulate ? *out + static_cast<float>(v) : static_cast<float>(v);
   }
 }
 
