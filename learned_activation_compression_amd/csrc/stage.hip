@@ -185,7 +185,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
     const int64_t n = n0 + threadIdx.x / TPR;
     const bool in = n < a.N;
     const int64_t at = (in ? n : 0) * a.d;
-    Fetch<T, MODE> fx[V], fy[V], fq[V], fg[V], fw[V];
+    Fetch<T, MODE> fx[V], fy[V], fg[V];
+    Fetch<T, MODE == kOdd ? kAny : MODE> fq[V], fw[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) fx[j].issue(a.X + at, col(j), a.d);
     if (a.Y) {
@@ -303,10 +304,10 @@ struct NormBwdArgs {
 //
 // Four tensors in, two out, and the three weights' sums in registers.  One row is
 // four dependent steps (load, sums, gX and the dot product of gY, gY), so the loads
-// of the next row are issued before this row's arithmetic: 16384 x 1024 bf16 in 39.8
-// us (5.1 TB/s), against 84 us with each row loaded when its turn comes.  512 blocks
+// of the next row are issued before this row's arithmetic: 16384 x 1024 bf16 in 40
+// us (5.0 TB/s), against 84 us with each row loaded when its turn comes.  512 blocks
 // are what the registers (135 a thread) keep resident; more would only add partial
-// rows to join (4.2 us for 512).
+// rows to join (4 us for 512).
 template <typename T, int TPR, int V, bool PRE, bool POST, bool MANY, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;

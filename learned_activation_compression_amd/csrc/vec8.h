@@ -12,6 +12,7 @@
 namespace mapl {
 
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
@@ -163,7 +164,10 @@ __device__ __forceinline__ void store8(float* p, const float* v, int left) {
 // The first three load without a branch, so that loads can stay in flight over
 // the arithmetic of an earlier row; Fetch keeps what was loaded until value().
 // Every address lies within the row.
-enum RowMode { kVec, kEven, kOdd, kTiny };
+//  kAny   d >= 8, one row that starts at a 4-byte boundary (a weight beside odd
+//         rows): only its last vector is at a 2-byte boundary, which the memory
+//         system takes too, at the price of that one access.
+enum RowMode { kVec, kEven, kOdd, kTiny, kAny };
 
 template <typename T, RowMode MODE>
 struct Fetch;
@@ -208,6 +212,16 @@ struct Fetch<bf16_t, kOdd> {
     const u32x4 e = {m[0], m[1], m[2], x | (y << 16)};
     const u32x4 o = {x | (m[0] << 16), (m[0] >> 16) | (m[1] << 16), (m[1] >> 16) | (m[2] << 16), (m[2] >> 16) | (y << 16)};
     return {shift_down(odd ? o : e, in ? static_cast<int>(min(max(c + 8 - d, int64_t(0)), int64_t(8))) : 8)};
+  }
+};
+template <>
+struct Fetch<bf16_t, kAny> {
+  u32x4 a;
+  __device__ __forceinline__ void issue(const bf16_t* row, int64_t c, int64_t d) {
+    a = *reinterpret_cast<const u32x4_a2*>(row + (c + 8 <= d ? c : d - 8));
+  }
+  __device__ __forceinline__ Raw8<bf16_t> value(int64_t c, int64_t d, bool in) const {
+    return {shift_down(a, in ? static_cast<int>(min(max(c + 8 - d, int64_t(0)), int64_t(8))) : 8)};
   }
 };
 template <>
