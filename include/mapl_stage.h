@@ -64,7 +64,7 @@ int stage_dropout(const void* X, void* Y, double p, uint64_t seed, uint64_t offs
  * X_out = res_scale * X (w_post, gate NULL and p = 0 then).  X_out NULL is not
  * stored; X_out and H may not both be NULL; w_pre is given exactly with H.
  * Outputs may not alias inputs, except that X_out may be X or Y.
- * eps > 0, finite; res_scale finite (MAPL_ERR_ARG); 1 <= d <= 8192,
+ * eps >= 2^-126, finite; res_scale finite (MAPL_ERR_ARG); 1 <= d <= 8192,
  * 0 <= N <= 2^31 - 1 (MAPL_ERR_SHAPE).
  * ---------------------------------------------------------------------- */
 int stage_norm(const void* X, const void* Y, const void* w_post, const void* gate, const void* w_pre, void* X_out,

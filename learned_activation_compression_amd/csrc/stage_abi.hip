@@ -2,7 +2,9 @@
 // The operations are documented in include/mapl_stage.h.
 #include "../../include/mapl_stage.h"
 
+#include <cfloat>
 #include <cmath>
+#include <initializer_list>
 
 #include "internal.h"
 
@@ -29,7 +31,8 @@ int check_norm_shape(int64_t N, int64_t d, int64_t gate_rows) {
 }
 
 int check_norm_scalars(float res_scale, float eps, double p) {
-  if (!std::isfinite(res_scale) || !(eps > 0.f) || !std::isfinite(eps) || !(p >= 0.0 && p <= 1.0)) return MAPL_ERR_ARG;
+  // a subnormal eps would count as zero in the reciprocal root of an empty row
+  if (!std::isfinite(res_scale) || !(eps >= FLT_MIN) || !std::isfinite(eps) || !(p >= 0.0 && p <= 1.0)) return MAPL_ERR_ARG;
   return MAPL_OK;
 }
 

@@ -286,3 +286,14 @@ def test_everything_dropped(dt):
     gx = rows(rng, 19, 333, dt)
     g = lac.stage_norm_bwd(gx, None, None, a["Y"], a["w_post"], a["gate"], None, p=1.0, seed=4)
     assert torch.equal(g[0], gx) and not g[1].any() and not g[2].any() and not g[3].any()
+
+
+def test_empty_rows_with_the_smallest_eps():
+    X = torch.zeros(5, 300, device=DEV)
+    X[3] = 1e-20
+    w = torch.ones(300, device=DEV)
+    eps = float(torch.finfo(torch.float32).tiny)
+    x, h = lac.stage_norm(X, X, w, None, w, eps=eps)
+    g = lac.stage_norm_bwd(X + 1, X, x, X, w, None, w, eps=eps)
+    assert x.isfinite().all() and h.isfinite().all() and not h[[0, 1, 2, 4]].any()
+    assert all(t.isfinite().all() for t in (g[0], g[2], g[4]))

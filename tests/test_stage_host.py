@@ -161,7 +161,7 @@ def test_norm_common_refusals(lib, call):
     assert call(lib, dt=9) == EDTYPE
     for bad in (dict(N=-1), dict(N=2 ** 31), dict(d=0), dict(d=8193), dict(G=-1), dict(N=10, G=3), dict(N=2, G=4)):
         assert call(lib, **bad) == ESHAPE, bad
-    for bad in (dict(eps=0.0), dict(eps=-1.0), dict(eps=float("inf")), dict(eps=float("nan")), dict(p=1.5),
+    for bad in (dict(eps=0.0), dict(eps=1e-39), dict(eps=-1.0), dict(eps=float("inf")), dict(eps=float("nan")), dict(p=1.5),
                 dict(p=float("nan")), dict(res_scale=float("inf")), dict(gate=None), dict(G=0),
                 dict(N=4, Y=None), dict(N=4, Y=None, p=0.0), dict(N=4, Y=None, p=0.0, w_post=None)):
         assert call(lib, **bad) == EARG, bad
