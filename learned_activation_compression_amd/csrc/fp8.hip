@@ -633,7 +633,9 @@ void join_t(const float* part, int splits, T* C, int64_t n, int accumulate, hipS
 }
 
 // How a product is cut (times: one MI355X, bf16 C unless stated):
-//  - few rows, M <= 128: k_fp8_few (128 x 2048 x 2048: 6.4 us, 64 x 64 tiles 6.7, 128 x 128 tiles 10);
+//  - few rows, M <= 64, and M <= 128 while K is below 8192: k_fp8_few (128 x 2048 x 2048: 6.4 us, 64 x 64 tiles
+//    6.7, 128 x 128 tiles 10; 20 x 4096 x 16384 fp32: 15.6 us, split tiles 22; but 100 x 4000 x 16000: 32 us, split
+//    tiles 20, as a block there goes through all of K);
 //  - 256 x 256 tiles where they fill the 256 CUs (4000 x 4096 x 4096: 52 us, 128 x 128 tiles 62);
 //  - 128 x 128 tiles from 160 of them (2000 x 2048 x 2048, 256 tiles: 12.4 us, 64 x 64 tiles 16): with two
 //    workgroups a CU and 2 stages each, or with one and 4 (2048 x 2048 x 8192: 35 us, with 2 stages 43);
@@ -654,7 +656,7 @@ Cut cut(int64_t M, int64_t N, int64_t K) {
   const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   const int64_t t128 = tiles(128), parts = std::min((2 * t128 <= kCus ? 1 : 2) * kCus / t128, KB / 16);
   Cut c{kFew, false, 1, KB};
-  if (M <= 128) return c;
+  if (M <= 64 || (M <= 128 && KB < 64)) return c;
   if (tiles(256) >= kCus) {
     c.kind = kTile256;
   } else if (t128 >= 160) {

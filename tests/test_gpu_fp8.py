@@ -66,7 +66,7 @@ def test_pack_extremes():
 
 SHAPES = [(1, 1, 1), (1, 32, 128), (7, 100, 5), (32, 64, 130), (33, 31, 1000), (64, 500, 256), (65, 129, 127),
           (128, 128, 128), (129, 257, 384), (200, 1000, 640), (300, 520, 2048), (1000, 96, 16), (16, 2048, 2048),
-          (1000, 1530, 1999), (520, 520, 9000), (16, 16, 16384)]
+          (1000, 1530, 1999), (520, 520, 9000), (16, 16, 16384), (64, 90, 9000), (100, 300, 8200), (128, 140, 8191)]
 
 
 @pytest.mark.parametrize("M, N, K", SHAPES)
