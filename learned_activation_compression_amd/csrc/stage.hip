@@ -609,7 +609,7 @@ struct BwdLaunch {
     });
   }
   static void go(const NormBwdArgs<T>& a, dim3 grid, hipStream_t s) {
-    if (!a.Y) return k<true, false, false>(a, grid, s);
+    if (!a.Y) return k<true, false, false>(a, grid, s);  // with gH (launch_stage_norm_bwd)
     if (a.sp.many) return a.gH ? k<true, true, true>(a, grid, s) : k<false, true, true>(a, grid, s);
     return a.gH ? k<true, true, false>(a, grid, s) : k<false, true, false>(a, grid, s);
   }
@@ -694,6 +694,10 @@ static void norm_bwd_t(const StageNorm& c, const StageNormGrads& g, hipStream_t 
 }
 
 void launch_stage_norm_bwd(const StageNorm& c, const StageNormGrads& g, int bf16, hipStream_t s) {
+  // neither norm nor block: X_out was res_scale X, and gX is res_scale gX_out, the same pass
+  if (!c.Y && !g.gH)
+    return launch_stage_norm({g.gX_out, nullptr, nullptr, nullptr, nullptr, g.gX, nullptr, c.res_scale, c.eps, 0.0, 0, 0,
+                              c.N, c.d, 0}, bf16, s);
   (bf16 ? norm_bwd_t<bf16_t> : norm_bwd_t<float>)(c, g, s);
 }
 
