@@ -88,7 +88,8 @@ int stage_norm(const void* X, const void* Y, const void* w_post, const void* gat
  * required exactly when its weight (w_post, gate; w_pre with gH) is given; gX
  * always, gY exactly when Y is.  gX_out without gH and Y: gX = res_scale gX_out.
  * With N = 0 each gradient given is zeroed.  The sums over rows have a fixed split and
- * order (no floating-point atomics): results are bitwise repeatable.  `ws` of
+ * order (no floating-point atomics): results are bitwise repeatable.  At most 512 rows
+ * add up in fp32 before their sums are joined in fp64, whatever N is.  `ws` of
  * stage_norm_bwd_workspace_bytes() holds the partial sums, 16-byte aligned
  * (MAPL_ERR_ARG); it may be NULL when that is 0.  gX may be gX_out and gY may
  * be gH or Y.  Other rules as for stage_norm. */

@@ -278,11 +278,12 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 // ------------------------------------------------------------------- backward --
 // The rows are split over blocks, and a block's rows over its slots, both into
 // contiguous runs, so that the sums over rows have a fixed order.
-//  - few gate rows (or no gate): a block's rows lie in one gate row; `bpg`
-//    blocks share a gate row.  Each block leaves one partial row of every
-//    weight gradient, and k_stage_norm_grads joins them.
-//  - many gate rows (a gate per token): a slot takes `gps` whole gate rows and
-//    writes their gradients itself.
+//  - few gate rows (or no gate), or gate rows of more than kBwdRun rows: a
+//    block's rows lie in one gate row; `bpg` blocks share a gate row.  Each block
+//    leaves one partial row of every weight gradient, and k_stage_norm_grads
+//    joins them.
+//  - many gate rows (a gate per token): a slot takes `gps` whole gate rows, of
+//    kBwdRun rows at most, and writes their gradients itself.
 struct BwdSplit {
   int64_t blocks, bpg, rows_per_block, gps;
   bool many;
@@ -498,13 +499,15 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a
 
 // Joins the partial rows: block (x, y) sums 32 columns of one output row, 4
 // columns by 32 runs of rows a thread, in a fixed order, in fp64: it costs nothing
-// here.  y = 0: w_post; 1: w_pre; 2 + g: gate row g.
+// here.  y = 0: w_post; 1: w_pre; 2 + g: gate row g, counted on over the grid's z.
+// (A loop over y in place of z takes 4 us more.)
 __global__ __launch_bounds__(256) void k_stage_norm_grads(const float* part, float* g_w_post, float* g_w_pre,
-                                                          float* g_gate, int64_t blocks, int64_t bpg, int d,
-                                                          int accumulate) {
+                                                          float* g_gate, int64_t blocks, int64_t bpg, int64_t gates,
+                                                          int d, int accumulate) {
   __shared__ double lds[32][33];
-  const int64_t y = int64_t(blockIdx.y);
-  float* out = y == 0 ? g_w_post : y == 1 ? g_w_pre : g_gate ? g_gate + (y - 2) * d : nullptr;
+  const int64_t y = int64_t(blockIdx.z) * gridDim.y + blockIdx.y;
+  if (y >= 2 + gates) return;
+  float* out = y == 0 ? g_w_post : y == 1 ? g_w_pre : g_gate + (y - 2) * d;
   if (out == nullptr) return;
   const float* src = part + (y == 0 ? 0 : y == 1 ? 2 * blocks : blocks + (y - 2) * bpg) * d;
   const int64_t rows = y < 2 ? blocks : bpg;
@@ -537,6 +540,10 @@ __global__ __launch_bounds__(256) void k_stage_norm_grads(const float* part, flo
 }
 
 constexpr int64_t kBwdBlocks = 512;
+// Rows that a slot adds up in fp32 before the sum is joined with others in fp64: the
+// error of a weight gradient is bounded by them, not by the number of rows.  More
+// rows than kBwdBlocks blocks hold that way take a multiple of the blocks.
+constexpr int64_t kBwdRun = 512;
 
 // slot shape of a width: TPR threads, V vectors of 8 columns each
 struct SlotShape {
@@ -561,14 +568,17 @@ SlotShape slot_shape(int64_t d, bool bwd) {
 BwdSplit bwd_split(int64_t N, int64_t d, int64_t gate_rows) {
   BwdSplit s{};
   const int64_t S = slots_per_block(slot_shape(d, true)), G = gate_rows > 0 ? gate_rows : 1, rpg = N / G;
-  s.many = G > kBwdBlocks;
+  const auto parts = [](int64_t n, int64_t of) { return (n + of - 1) / of; };
+  s.many = G > kBwdBlocks && rpg <= kBwdRun;
   if (s.many) {
-    s.gps = (G + kBwdBlocks * S - 1) / (kBwdBlocks * S);
-    s.blocks = (G + s.gps * S - 1) / (s.gps * S);
+    const int64_t turns = parts(parts(G, kBwdBlocks * S) * rpg, kBwdRun);
+    s.gps = std::min(parts(G, kBwdBlocks * S * turns), kBwdRun / rpg);
+    s.blocks = parts(G, s.gps * S);
     return s;
   }
-  s.bpg = std::max<int64_t>(1, std::min(kBwdBlocks / G, (rpg + S - 1) / S));
-  s.rows_per_block = (rpg + s.bpg - 1) / s.bpg;
+  s.bpg = std::max<int64_t>(1, std::min(kBwdBlocks / G, parts(rpg, S)));
+  s.bpg *= parts(parts(rpg, s.bpg * S), kBwdRun);
+  s.rows_per_block = parts(rpg, s.bpg);
   s.blocks = G * s.bpg;
   return s;
 }
@@ -686,10 +696,11 @@ static void norm_bwd_t(const StageNorm& c, const StageNormGrads& g, hipStream_t 
   a.accumulate = g.accumulate;
   by_shape<T, BwdLaunch, true>(slot_shape(c.d, true), a, dim3(uint32_t(a.sp.blocks)), s);
   if (c.w_post || c.gate || g.gH) {
-    const uint32_t gates = c.gate && !a.sp.many ? uint32_t(c.gate_rows) : 0;
-    hipLaunchKernelGGL(k_stage_norm_grads, dim3(uint32_t((c.d + 31) / 32), 2 + gates), dim3(256), 0, s, g.ws,
+    const int64_t gates = c.gate && !a.sp.many ? c.gate_rows : 0;
+    const uint32_t ny = uint32_t(std::min<int64_t>(2 + gates, 32768)), nz = uint32_t((2 + gates + ny - 1) / ny);
+    hipLaunchKernelGGL(k_stage_norm_grads, dim3(uint32_t((c.d + 31) / 32), ny, nz), dim3(256), 0, s, g.ws,
                        c.w_post ? g.g_w_post : nullptr, g.gH ? g.g_w_pre : nullptr, gates ? g.g_gate : nullptr,
-                       a.sp.blocks, a.sp.bpg, a.d, g.accumulate);
+                       a.sp.blocks, a.sp.bpg, gates, a.d, g.accumulate);
   }
 }
 
