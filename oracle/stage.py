@@ -138,3 +138,14 @@ def round_blocks(X, square=False):
             y[fin] = e4m3(x[fin] * 2.0 ** -s) * 2.0 ** s
             out[r0:r0 + b, c0:c0 + 128] = y
     return out
+
+
+def cut_products(a, b):
+    """a b^T where, of each 8 columns' products, those bits count that are at
+    least 2^-13 of the power of two at or below the largest of the 8."""
+    M, K = a.shape
+    p = a[:, None, :] * b[None, :, :]
+    p = np.concatenate([p, np.zeros((M, b.shape[0], -K % 8))], axis=2).reshape(M, b.shape[0], -1, 8)
+    top = np.abs(p).max(axis=3, keepdims=True)
+    q = 2.0 ** (np.floor(np.log2(np.where(top > 0, top, 1.0))) - 13)
+    return np.sum(np.trunc(p / q) * q, axis=(2, 3))
