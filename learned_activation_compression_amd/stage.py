@@ -85,6 +85,8 @@ def _elsewhere(like, name, stream) -> bool:
 
 @contextlib.contextmanager
 def _there(like, stream):
+    if stream is not None and stream.device != like.device:
+        raise MaplError(-1, "binding", f"the stream is on {stream.device}, the tensors on {like.device}")
     with torch.cuda.device(like.device):
         if stream is None:
             yield

@@ -27,3 +27,13 @@ def test_backward_of_the_scaled_residual_alone(dt):
     # with a gradient of H each of its tensors is needed
     assert bwd(gH=FAKE) == ENULL and bwd(gH=FAKE, w_pre=FAKE, g_w_pre=FAKE) == ENULL
     assert bwd(gH=FAKE, X_out=FAKE, w_pre=FAKE, g_w_pre=FAKE) == ENULL  # no workspace
+
+
+def test_a_stream_of_another_device_is_refused():
+    # entering it would leave the tensors' device, and the call would then run on that device's current stream instead
+    from types import SimpleNamespace
+    like = SimpleNamespace(device=torch.device("cuda", 0))
+    with pytest.raises(lac.MaplError) as e:
+        with binding._there(like, SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)):
+            pass
+    assert e.value.status == -1 and "cuda:1" in str(e.value) and "cuda:0" in str(e.value)
