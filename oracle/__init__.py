@@ -17,10 +17,12 @@ Modules
   rvq    Section 3.5 residual multi-codebook VQ encode / decode and the
          streaming codebook sync of Appendix F (algorithm steps).
   stage  the operators of the stage around the boundary: dropout, block edge,
-         8-bit rounding (plain definitions, pinned by tests/test_stage_host.py).
+         8-bit rounding (plain definitions).
 
-Parity status: every function here is pinned by tests/test_oracle_pins.py
-(brute-force loops, closed forms via the SVD, invariants stated on the pages,
-library special cases and the paper's printed payload sizes).
+Parity status: the functions of codec, spel and rvq are pinned by
+tests/test_oracle_pins.py (brute-force loops, closed forms via the SVD,
+invariants stated on the pages, library special cases and the paper's printed
+payload sizes), those of stage by tests/test_stage_host.py (published answers,
+differences, the library's cast) and tests/test_stage_products.py (by hand).
 """
 from . import codec, spel, rvq, stage  # noqa: F401

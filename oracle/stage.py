@@ -142,10 +142,14 @@ def round_blocks(X, square=False):
 
 def cut_products(a, b):
     """a b^T where, of each 8 columns' products, those bits count that are at
-    least 2^-13 of the power of two at or below the largest of the 8."""
-    M, K = a.shape
-    p = a[:, None, :] * b[None, :, :]
-    p = np.concatenate([p, np.zeros((M, b.shape[0], -K % 8))], axis=2).reshape(M, b.shape[0], -1, 8)
-    top = np.abs(p).max(axis=3, keepdims=True)
-    q = 2.0 ** (np.floor(np.log2(np.where(top > 0, top, 1.0))) - 13)
-    return np.sum(np.trunc(p / q) * q, axis=(2, 3))
+    least 2^-13 of 2^e, e the largest sum of two factors' exponents among the 8."""
+    def exponent(x):
+        return np.where(x != 0, np.frexp(x)[1] - 1, -10000)
+
+    def by_eights(x):
+        return np.concatenate([x, np.zeros(x.shape[:1] + (-x.shape[1] % 8,))], axis=1).reshape(x.shape[0], -1, 8)
+
+    a, b = by_eights(a)[:, None], by_eights(b)[None]
+    e = np.max(exponent(a) + exponent(b), axis=3, keepdims=True)
+    q = np.ldexp(1.0, np.maximum(e, -1000) - 13)
+    return np.sum(np.trunc(a * b / q) * q, axis=(2, 3))

@@ -138,3 +138,12 @@ def test_a_small_product_beside_a_large_one():
     assert exact.diagonal()[:4].tolist() == [4.0, 4.0, -12.0, 0.0]
     assert bf.diagonal()[:4].tolist() == [0.0, 4.0, -8.0, 0.0]
     assert torch.equal(bf.double(), torch.from_numpy(stage.cut_products(a, b)))
+
+
+def test_the_cut_follows_the_exponents_of_the_factors():
+    A, B = torch.zeros(4, 128, device=DEV), torch.zeros(4, 128, device=DEV)
+    A[:, 0], A[:, 1], B[:, 0], B[:, 1] = 448.0, 448.0, 448.0, -448.0  # 3.0625 * 2^16: cut at 2^(16 - 13)
+    A[:, 2], B[:, 2] = torch.tensor([3.0, 2.0, 2.0, 7.0], device=DEV), torch.tensor([4.0, 4.0, 2.0, -4.0], device=DEV)
+    got = lac.fp8_gemm(*packs(A, B), 4, 4, 128).double().cpu()
+    assert torch.equal(got, torch.from_numpy(stage.cut_products(A.cpu().double().numpy(), B.cpu().double().numpy())))
+    assert got.diagonal().tolist() == [8.0, 8.0, 0.0, -24.0]

@@ -41,3 +41,9 @@ def test_small_terms_beside_cancelling_large_ones_show_a_cut():
     for k in range(K):
         s += (a[:, k, None] * b[None, :, k]).astype(np.float32)
     assert np.array_equal(s, exact)
+
+
+def test_the_cut_follows_the_exponents_not_the_product():
+    a, b = np.zeros((1, 8)), np.zeros((1, 8))
+    a[0, :3], b[0, :3] = [448, 448, 3], [448, -448, 4]  # 448 * 448 is 3.0625 * 2^16
+    assert stage.cut_products(a, b) == 8
