@@ -133,9 +133,12 @@ int fp8_unpack(const void* pk, size_t pk_bytes, void* X, int64_t rows, int64_t c
 /* C [M][N] (+)= A B^T for packs A of [M][K] and B of [N][K], rounded once to
  * `dt`.  An fp32 C has fp32 sums of exact products (operand values below 2^-126
  * may count as zero).  A bf16 C comes from the e4m3 matrix instruction, twice as
- * fast, which keeps 13 bits below the largest of a few neighbouring products
- * before they enter its fp32 accumulator: about 1.5e-5 of the sum's size, far
- * below the output's rounding (2^-8).  accumulate = 1 adds into an fp32 C
+ * fast, which cuts the products of each 8 columns towards zero to 13 bits below the
+ * largest of them before they enter its fp32 accumulator: off by less than 8.5e-4 of
+ * the sum of absolute values at worst, and, as the cuts of products of random sign
+ * average out, by 1.6e-5 of it at K = 64, 2e-6 at K = 1024.  That is far below the
+ * output's rounding (2^-8) unless a sum cancels to a small part of its terms; where
+ * that matters, ask for an fp32 C.  accumulate = 1 adds into an fp32 C
  * (MAPL_ERR_ARG for bf16, which would round twice).  Few output tiles with a
  * long K are split over K; the partial sums go to `ws` of
  * fp8_gemm_workspace_bytes() (may be NULL when that is 0; 16-byte aligned) and

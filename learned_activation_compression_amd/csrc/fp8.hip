@@ -258,6 +258,8 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
   return (c & 0x80u) ? -v : v;
 }
 
+// For looking at packs, not for a step's path: one element a store (16384 x 1024 to
+// bf16 in 46 us, to fp32 in 140 us; 10 and 16 us of traffic).
 template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_unpack(View p, T* X, int64_t rows, int64_t cols) {
   const uint32_t nkb = static_cast<uint32_t>(p.KB);
@@ -332,11 +334,14 @@ struct GemmArgs {
 // so a lane's accumulators run along a row of C.
 //
 // Two ways to multiply, by the output's type (EXACT):
-//  - bf16: the scaled e4m3 matrix instruction, 2.0x the rate of the other.  It
-//    aligns the products of a few neighbouring columns to the largest of them and
-//    keeps 13 bits below it before they enter the fp32 accumulator: 1.5e-5 of the
-//    sum's size on normal data (measured, any K), against 2^-8 for the output's
-//    own rounding and 2^-4 for that of the codes.
+//  - bf16: the scaled e4m3 matrix instruction, 2.0x the rate of the other.  Before
+//    they enter the fp32 accumulator it cuts the products of each 8 columns,
+//    towards zero, to multiples of 2^(e - 13), e the largest sum of two factors'
+//    exponents among the 8 (measured with factors placed one by one): less than
+//    7 2^-13 = 8.5e-4 of the sum of absolute values at worst.  On data of random
+//    sign that averages out: 1.6e-5 of it at K = 64, 2.0e-6 at 1024, 7e-7 at 8192
+//    (the largest of 65536 outputs, beyond their rounding), against 2^-8 of the
+//    output for its own rounding and 2^-4 for that of the codes.
 //  - fp32 (weight gradients): the codes times their scales are widened to bf16,
 //    which holds them exactly, and go through the bf16 instruction, whose sums
 //    are fp32 throughout (1e-8 on the same data).
@@ -375,8 +380,8 @@ __device__ __forceinline__ void put16(float* c, const char* src, int left, int a
 // 8192 x 8192 x 8192: 389 us, 2830 TFLOP/s, where MFMAs alone on zeros reach 5000.
 // Without the copies (the same operands over and over) 4096 x 4096 x 8192 takes 90
 // instead of 101 us, without the reads from LDS 99: the matrix cores are the bound,
-// at the clock that random data leaves them.  32768 x 8192 x 2048 takes 530 us, as
-// its 512 MB of C leave in bursts; 128 x 256 tiles, two workgroups a CU, spread them
+// at the clock that random data leaves them.  32768 x 8192 x 2048 takes 520 to 555 us,
+// as its 512 MB of C leave in bursts; 128 x 256 tiles, two workgroups a CU, spread them
 // and gain nothing (565 us).  Widened operands (EXACT): 8192 x 8192 x 4096 in 400 us,
 // 1370 TFLOP/s.
 template <typename T, bool EXACT, int WM, int WN, int FM, int FN, int NS>
@@ -632,7 +637,8 @@ void join_t(const float* part, int splits, T* C, int64_t n, int accumulate, hipS
                      splits, C, n, accumulate);
 }
 
-// How a product is cut (times: one MI355X, bf16 C unless stated):
+// How a product is cut (times: one MI355X, bf16 C unless stated, the same operands
+// again and again, as far as they fit in the last-level cache):
 //  - few rows, M <= 64, and M <= 128 while K is below 8192: k_fp8_few (128 x 2048 x 2048: 6.4 us, 64 x 64 tiles
 //    6.7, 128 x 128 tiles 10; 20 x 4096 x 16384 fp32: 15.6 us, split tiles 22; but 100 x 4000 x 16000: 32 us, split
 //    tiles 20, as a block there goes through all of K);

@@ -306,9 +306,10 @@ struct NormBwdArgs {
 // Four tensors in, two out, and the three weights' sums in registers.  One row is
 // four dependent steps (load, sums, gX and the dot product of gY, gY), so the loads
 // of the next row are issued before this row's arithmetic: 16384 x 1024 bf16 in 40
-// us (5.0 TB/s), against 84 us with each row loaded when its turn comes.  512 blocks
-// are what the registers (135 a thread) keep resident; more would only add partial
-// rows to join (4 us for 512).
+// us (5.0 TB/s), against 84 us with each row loaded when its turn comes.  512 blocks,
+// two a CU (three would fit a CU's registers at that width): with 768 and 1024 of
+// them the call takes 40.3 and 44.1 instead of 39.7 us, for 8192 x 2048 41.2 and
+// 45.2 instead of 39.0 (the same tensors again and again).
 template <typename T, int TPR, int V, bool PRE, bool POST, bool MANY, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_bwd(NormBwdArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
@@ -561,7 +562,9 @@ SlotShape slot_shape(int64_t d, bool bwd) {
   if (d <= 1536) return {192, 1};
   if (d <= 2048) return {256, 1};
   if (d <= 4096) return {512, 1};
-  // a backward row does not fit the 128 registers that 1024 threads have each (4096 x 8192 bf16: 222 against 103 us)
+  // a backward row does not fit the 128 registers that 1024 threads have each (4096 x 8192: bf16 192 against 93 us, fp32
+  // 348 against 211; 4096 x 8191 bf16: 300 against 142).  With two vectors a thread fp32, odd rows and a gate per token
+  // still spill, up to 344 bytes a thread.
   return bwd ? SlotShape{512, 2} : SlotShape{1024, 1};
 }
 

@@ -1,7 +1,7 @@
 // Rows of any width and tensors of any offset, 8 consecutive elements at a time.
 // The memory system takes 16 bytes at any 4-byte boundary; what rows of other
 // widths need beyond that depends on the width and the addresses, so kernels come
-// in the four forms of RowMode and the launch picks one.
+// in the first four forms of RowMode and the launch picks one.
 #pragma once
 
 #include <initializer_list>
@@ -164,9 +164,10 @@ __device__ __forceinline__ void store8(float* p, const float* v, int left) {
 // The first three load without a branch, so that loads can stay in flight over
 // the arithmetic of an earlier row; Fetch keeps what was loaded until value().
 // Every address lies within the row.
-//  kAny   d >= 8, one row that starts at a 4-byte boundary (a weight beside odd
-//         rows): only its last vector is at a 2-byte boundary, which the memory
-//         system takes too, at the price of that one access.
+//  kAny   d >= 8, one row that all others share (a weight beside odd rows), at any
+//         address: 16 bytes in one access, which the compiler and the memory system
+//         take at 2-byte boundaries too, at a price.  From a 4-byte boundary only
+//         the last vector pays it, otherwise each, out of the caches.
 enum RowMode { kVec, kEven, kOdd, kTiny, kAny };
 
 template <typename T, RowMode MODE>
