@@ -1,0 +1,75 @@
+/*
+ * mapl_block.h -- C ABI of the operators between a pipeline stage's boundary and
+ * its loss: attention over packed sequences, with its backward pass.  Same library
+ * and conventions as mapl.h and mapl_stage.h: device pointers owned by the caller, no
+ * allocation, work enqueued on `stream` without synchronising, host validation before
+ * anything is enqueued, status codes MAPL_OK / MAPL_ERR_*.  Pointers need the
+ * alignment of their element type only, except workspaces (16 bytes).  `dt`
+ * (MAPL_BF16 or MAPL_F32) is the storage type of every floating-point tensor
+ * unless stated otherwise; sums, softmax statistics and norms are fp32, each output
+ * is rounded once to its type, nearest even.
+ */
+#ifndef MAPL_BLOCK_H
+#define MAPL_BLOCK_H
+
+#include "mapl_stage.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------------
+ * Causal attention over packed sequences, grouped heads.
+ *
+ * The rows 0 .. N - 1 hold S sequences one behind the other: sequence s has the
+ * rows cu[s] .. cu[s + 1] - 1 (cu [S + 1], int32, on the device, ascending, within
+ * [0, N]; a sequence may be empty).  Query head h reads key head h / (Hq / Hkv).
+ * Row i sees the rows j of its own sequence up to itself, start(i) <= j <= i:
+ *
+ *   s_ij  = scale * q_i . k_j
+ *   lse_i = log sum_j exp(s_ij)                              (natural)
+ *   o_i   = sum_j exp(s_ij - lse_i) v_j
+ *
+ * Q, O are N rows of Hq heads of D values, K, V of Hkv heads; row n of a tensor
+ * begins at n times its leading dimension (ldq >= Hq D, ... ; in elements), so that
+ * the three may be columns of one fused projection.  lse [Hq][N], fp32.  Rows
+ * outside the sequences are neither read into a result nor written.  What a row
+ * does not see never reaches it, infinities and NaN included; among what it sees
+ * they act as in the formula (a row that sees only scores of -inf is NaN).
+ * bf16: the weights exp(s_ij - m), m near the row's largest score, are rounded to
+ * bf16 for the product with V, their sum is not.
+ *
+ * 1 <= D <= 128, Hkv >= 1 divides Hq, S >= 0, N >= 0, N Hq <= 2^30, leading
+ * dimensions to 2^31 - 1 (MAPL_ERR_SHAPE); scale > 0, finite (MAPL_ERR_ARG).
+ * Outputs may not overlap inputs.
+ * The edges are data on the device and are not checked; edges that break the rules
+ * give wrong rows, and never an access outside the tensors' N rows.
+ * ---------------------------------------------------------------------- */
+int stage_attn(const void* Q, const void* K, const void* V, const int32_t* cu, void* O, float* lse, float scale,
+               int64_t S, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t ldq, int64_t ldk, int64_t ldv,
+               int64_t ldo, mapl_dtype dt, hipStream_t stream);
+
+/* Backward of stage_attn, from its inputs and its stored O and lse, given gO = dL/dO:
+ *
+ *   p_ij  = exp(s_ij - lse_i),  delta_i = gO_i . o_i
+ *   ds_ij = p_ij (gO_i . v_j - delta_i)
+ *   gQ_i  = scale sum_j ds_ij k_j
+ *   gK_j  = scale sum_h sum_i ds_ij q_i,  gV_j = sum_h sum_i p_ij gO_i
+ *
+ * with h over the query heads that read the key head.  bf16: p_ij and ds_ij are
+ * rounded to bf16 for the products; the sums over rows and heads are fp32 and each
+ * gradient is rounded once.  Sums have a fixed order: results are bitwise
+ * repeatable.  `ws` of stage_attn_bwd_workspace_bytes(), 16-byte aligned.  Other rules
+ * as for stage_attn. */
+size_t stage_attn_bwd_workspace_bytes(int64_t N, int64_t Hq, int64_t Hkv, int64_t D);
+int stage_attn_bwd(const void* gO, const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                   const int32_t* cu, void* gQ, void* gK, void* gV, float scale, int64_t S, int64_t N, int64_t Hq,
+                   int64_t Hkv, int64_t D, int64_t ldgo, int64_t ldq, int64_t ldk, int64_t ldv, int64_t ldo,
+                   int64_t ldgq, int64_t ldgk, int64_t ldgv, mapl_dtype dt, void* ws, size_t ws_bytes,
+                   hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MAPL_BLOCK_H */

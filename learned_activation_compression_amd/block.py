@@ -1,0 +1,143 @@
+"""Binding of the operators between a stage's boundary and its loss
+(include/mapl_block.h): causal attention over packed sequences with its backward
+pass.
+
+As in the rest of the package each function has the name of the C entry point
+it wraps and marshals arguments only.  Outputs and workspaces that are not given
+are allocated on the stream that the call runs on, so with an explicit `stream`
+the caller orders the inputs, and nothing else, against it.
+"""
+from __future__ import annotations
+
+import functools
+import os
+import re
+
+import torch
+
+from . import HEADER_PATH, MaplError, _check, _dev, _dt, _f32, _i32, _i64, _sz, _vp
+from . import load as _load
+from .stage import _bytes, _elsewhere, _ptr, _raw_stream, _there
+
+__all__ = ["stage_attn", "stage_attn_bwd_workspace_bytes", "stage_attn_bwd"]
+
+BLOCK_HEADER_PATH = os.path.join(os.path.dirname(HEADER_PATH), "mapl_block.h")
+
+_BLOCK_SIGS = {
+    "stage_attn": (_i32, [_vp] * 6 + [_f32] + [_i64] * 9 + [_i32, _vp]),
+    "stage_attn_bwd_workspace_bytes": (_sz, [_i64] * 4),
+    "stage_attn_bwd": (_i32, [_vp] * 10 + [_f32] + [_i64] * 13 + [_i32, _vp, _sz, _vp]),
+}
+
+_lib = None
+
+
+def _block_lib():
+    global _lib
+    if _lib is None:
+        lib = _load()
+        for name, (res, args) in _BLOCK_SIGS.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+def block_symbols() -> list:
+    """Names of the functions declared in include/mapl_block.h."""
+    with open(BLOCK_HEADER_PATH) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    return re.findall(r"^\s*(?:int|size_t)\s+([a-z][a-z0-9_]*)\s*\(", text, flags=re.M)
+
+
+# --------------------------------------------------------------- attention --
+
+def _heads(t, name, index, dtype=None, shape=None):
+    """Pointer and leading dimension of rows of heads [N, H, D]: heads lie side by side, rows at any stride."""
+    try:
+        if t.get_device() == index and (dtype is None or t.dtype is dtype) and t.dim() == 3:
+            N, H, D = t.shape
+            row, head, one = t.stride()
+            if shape is None or t.shape == shape:
+                # torch gives any stride to an axis of one
+                if (one == 1 or D == 1) and (head == D or H == 1) and (row >= H * D or N <= 1):
+                    return t.data_ptr(), row if N > 1 else H * D
+                raise MaplError(-2, "binding", f"{name}: heads must lie side by side and rows apart, strides are {t.stride()}")
+            raise MaplError(-2, "binding", f"{name} must be {list(shape)}, got {list(t.shape)}")
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MaplError(-1, "binding", f"{name} must be a device tensor")
+    if t.get_device() != index:
+        raise MaplError(-1, "binding", f"{name} is on {t.device}, not cuda:{index}")
+    if dtype is not None and t.dtype is not dtype:
+        raise MaplError(-3, "binding", f"{name} must be {dtype}, got {t.dtype}")
+    raise MaplError(-2, "binding", f"{name} must be [N, heads, D], got {list(t.shape)}")
+
+
+def _attn_shape(Q, K):
+    if not isinstance(Q, torch.Tensor) or not isinstance(K, torch.Tensor):
+        raise MaplError(-1, "binding", "Q and K must be torch.Tensors")
+    if Q.dim() != 3 or K.dim() != 3:
+        raise MaplError(-2, "binding", "Q and K must be [N, heads, D]")
+    return (*Q.shape, K.shape[1])
+
+
+def stage_attn(Q, K, V, cu, scale=None, O=None, lse=None, stream=None):
+    """Causal attention over packed sequences.  Q [N, Hq, D], K and V
+    [N, Hkv, D], rows at any stride (columns of a fused projection); cu [S + 1]
+    int32, the sequences' edges; scale defaults to D ** -0.5.  Returns (O, lse):
+    [N, Hq, D] and fp32 [Hq, N].  Rows outside the sequences are not written."""
+    if _elsewhere(cu, "cu", stream):
+        with _there(cu, stream):
+            return stage_attn(Q, K, V, cu, scale, O, lse)
+    N, Hq, D, Hkv = _attn_shape(Q, K)
+    dev, dt = cu.get_device(), Q.dtype
+    if O is None:
+        O = torch.empty((N, Hq, D), dtype=dt, device=cu.device)
+    if lse is None:
+        lse = torch.empty((Hq, N), dtype=torch.float32, device=cu.device)
+    q, ldq = _heads(Q, "Q", dev)
+    k, ldk = _heads(K, "K", dev, dt, (N, Hkv, D))
+    v, ldv = _heads(V, "V", dev, dt, (N, Hkv, D))
+    o, ldo = _heads(O, "O", dev, dt, (N, Hq, D))
+    _check(_block_lib().stage_attn(
+        q, k, v, _ptr(cu, "cu", dev, torch.int32), o, _ptr(lse, "lse", dev, torch.float32, (Hq, N)),
+        D ** -0.5 if scale is None else float(scale), cu.numel() - 1, N, Hq, Hkv, D, ldq, ldk, ldv, ldo, _dt(Q),
+        _raw_stream(dev)), "stage_attn")
+    return O, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def stage_attn_bwd_workspace_bytes(N: int, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace of stage_attn_bwd for these sizes."""
+    return int(_block_lib().stage_attn_bwd_workspace_bytes(N, Hq, Hkv, D))
+
+
+def stage_attn_bwd(gO, Q, K, V, O, lse, cu, scale=None, gQ=None, gK=None, gV=None, ws=None, stream=None):
+    """Backward of stage_attn from its inputs, O and lse.  Returns (gQ, gK, gV);
+    given ones may be columns of the fused projection's gradient."""
+    if _elsewhere(cu, "cu", stream):
+        with _there(cu, stream):
+            return stage_attn_bwd(gO, Q, K, V, O, lse, cu, scale, gQ, gK, gV, ws)
+    N, Hq, D, Hkv = _attn_shape(Q, K)
+    dev, dt = cu.get_device(), Q.dtype
+    new = lambda H: torch.empty((N, H, D), dtype=dt, device=cu.device)  # noqa: E731
+    gQ = new(Hq) if gQ is None else gQ
+    gK = new(Hkv) if gK is None else gK
+    gV = new(Hkv) if gV is None else gV
+    go, ldgo = _heads(gO, "gO", dev, dt, (N, Hq, D))
+    q, ldq = _heads(Q, "Q", dev)
+    k, ldk = _heads(K, "K", dev, dt, (N, Hkv, D))
+    v, ldv = _heads(V, "V", dev, dt, (N, Hkv, D))
+    o, ldo = _heads(O, "O", dev, dt, (N, Hq, D))
+    gq, ldgq = _heads(gQ, "gQ", dev, dt, (N, Hq, D))
+    gk, ldgk = _heads(gK, "gK", dev, dt, (N, Hkv, D))
+    gv, ldgv = _heads(gV, "gV", dev, dt, (N, Hkv, D))
+    ws, ws_ptr, ws_size = _bytes(ws, stage_attn_bwd_workspace_bytes(N, Hq, Hkv, D), "ws", cu)
+    _check(_block_lib().stage_attn_bwd(
+        go, q, k, v, o, _ptr(lse, "lse", dev, torch.float32, (Hq, N)), _ptr(cu, "cu", dev, torch.int32), gq, gk, gv,
+        D ** -0.5 if scale is None else float(scale), cu.numel() - 1, N, Hq, Hkv, D, ldgo, ldq, ldk, ldv, ldo, ldgq,
+        ldgk, ldgv, _dt(Q), ws_ptr, ws_size, _raw_stream(dev)), "stage_attn_bwd")
+    return gQ, gK, gV

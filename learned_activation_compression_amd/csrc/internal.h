@@ -171,4 +171,18 @@ size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 void launch_fp8_gemm(const uint8_t* A, const uint8_t* B, void* C, int accumulate, int64_t M, int64_t N, int64_t K,
                      int bf16, float* ws, hipStream_t s);
 
+// ---- operators between a stage's edge and its loss (include/mapl_block.h)
+struct Attn {  // leading dimensions in elements; the forward call leaves the gradients unset, the backward `out`
+  const void *Q, *K, *V, *O, *gO;
+  void *out, *gQ, *gK, *gV;
+  const int32_t* cu;
+  float *lse, *rows;
+  int64_t ldq, ldk, ldv, ldo, ldgo, ldgq, ldgk, ldgv;
+  float scale;
+  int64_t S, N, Hq, Hkv, D;
+};
+void launch_attn(const Attn& c, int bf16, hipStream_t s);
+size_t attn_bwd_ws_bytes(int64_t N, int64_t Hq, int64_t Hkv, int64_t D);
+void launch_attn_bwd(const Attn& c, int bf16, hipStream_t s);
+
 }  // namespace mapl
