@@ -11,8 +11,8 @@ The method is that of "Learned Subspace Compression for Communication-
 Efficient Pipeline Parallelism" (MAPL): Eq. (1)-(3) codec, its backward, the
 residual VQ of Section 3.5 with the streaming sync of Appendix F, and the SPEL
 projector update of Section 3.3.  The operators of the stage on either side of the boundary (block
-edge, dropout, 8-bit products) are in ``stage``, those between its projections and its loss (attention)
-in ``block``; both are exported here as well.
+edge, dropout, 8-bit products) are in ``stage``, those between its boundary and its loss (8-bit
+block edge, attention, distillation loss) in ``block``; both are exported here as well.
 """
 from __future__ import annotations
 
@@ -32,7 +32,8 @@ __all__ = [
     "MAPL_F32", "MAPL_BF16",
     "stage_dropout", "stage_norm", "stage_norm_bwd_workspace_bytes", "stage_norm_bwd",
     "fp8_pack_bytes", "fp8_pack", "fp8_unpack", "fp8_gemm_workspace_bytes", "fp8_gemm",
-    "stage_attn", "stage_attn_bwd_workspace_bytes", "stage_attn_bwd",
+    "stage_norm_pack", "stage_attn", "stage_attn_bwd_workspace_bytes", "stage_attn_bwd",
+    "stage_distill_workspace_bytes", "stage_distill", "stage_distill_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -523,5 +524,6 @@ from .stage import (  # noqa: E402,F401
 )
 # operators between a stage's boundary and its loss (include/mapl_block.h)
 from .block import (  # noqa: E402,F401
-    stage_attn, stage_attn_bwd_workspace_bytes, stage_attn_bwd,
+    stage_norm_pack, stage_attn, stage_attn_bwd_workspace_bytes, stage_attn_bwd,
+    stage_distill_workspace_bytes, stage_distill, stage_distill_bwd,
 )

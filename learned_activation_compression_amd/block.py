@@ -1,6 +1,7 @@
 """Binding of the operators between a stage's boundary and its loss
-(include/mapl_block.h): causal attention over packed sequences with its backward
-pass.
+(include/mapl_block.h): the block edge with an 8-bit output, causal attention over
+packed sequences and the distillation loss, the latter two with their backward
+passes.
 
 As in the rest of the package each function has the name of the C entry point
 it wraps and marshals arguments only.  Outputs and workspaces that are not given
@@ -15,18 +16,25 @@ import re
 
 import torch
 
-from . import HEADER_PATH, MaplError, _check, _dev, _dt, _f32, _i32, _i64, _sz, _vp
+from . import HEADER_PATH, MaplError, _check, _dt, _f32, _i32, _i64, _sz, _vp
 from . import load as _load
-from .stage import _bytes, _elsewhere, _ptr, _raw_stream, _there
+from .stage import _bytes, _elsewhere, _f64, _ptr, _raw_stream, _rows, _there, _u, _u64, fp8_pack_bytes
 
-__all__ = ["stage_attn", "stage_attn_bwd_workspace_bytes", "stage_attn_bwd"]
+__all__ = [
+    "stage_norm_pack", "stage_attn", "stage_attn_bwd_workspace_bytes", "stage_attn_bwd",
+    "stage_distill_workspace_bytes", "stage_distill", "stage_distill_bwd",
+]
 
 BLOCK_HEADER_PATH = os.path.join(os.path.dirname(HEADER_PATH), "mapl_block.h")
 
 _BLOCK_SIGS = {
+    "stage_norm_pack": (_i32, [_vp] * 8 + [_sz, _f32, _f32, _f64, _u64, _u64, _i64, _i64, _i64, _i32, _vp]),
     "stage_attn": (_i32, [_vp] * 6 + [_f32] + [_i64] * 9 + [_i32, _vp]),
     "stage_attn_bwd_workspace_bytes": (_sz, [_i64] * 4),
     "stage_attn_bwd": (_i32, [_vp] * 10 + [_f32] + [_i64] * 13 + [_i32, _vp, _sz, _vp]),
+    "stage_distill_workspace_bytes": (_sz, [_i64, _i64]),
+    "stage_distill": (_i32, [_vp] * 6 + [_f32] * 3 + [_i64] * 3 + [_i32, _vp, _sz, _vp]),
+    "stage_distill_bwd": (_i32, [_vp] * 7 + [_f32] * 3 + [_i64] * 3 + [_i32, _vp]),
 }
 
 _lib = None
@@ -49,6 +57,34 @@ def block_symbols() -> list:
     with open(BLOCK_HEADER_PATH) as f:
         text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
     return re.findall(r"^\s*(?:int|size_t)\s+([a-z][a-z0-9_]*)\s*\(", text, flags=re.M)
+
+
+# -------------------------------------------------------------- block edge --
+
+def stage_norm_pack(X, Y=None, w_post=None, gate=None, w_pre=None, res_scale=1.0, eps=1e-5, p=0.0, seed=0, offset=0,
+                    X_out=None, H=None, pkH=None, store_x=True, store_h=False, stream=None):
+    """stage_norm whose H leaves as the 8-bit operand [N][d] of fp8_gemm, packed
+    from H before its rounding.  Returns (X_out, H, pkH); X_out is None with
+    store_x = False, H is None unless it is given or store_h = True."""
+    if _elsewhere(X, "X", stream):
+        with _there(X, stream):
+            return stage_norm_pack(X, Y, w_post, gate, w_pre, res_scale, eps, p, seed, offset, X_out, H, pkH, store_x,
+                                   store_h)
+    N, d = _rows(X, "X")
+    dt, shape, dev = X.dtype, X.shape, X.get_device()
+    if X_out is None and store_x:
+        X_out = torch.empty_like(X)
+    if H is None and store_h:
+        H = torch.empty_like(X)
+    pkH, pk_ptr, pk_size = _bytes(pkH, fp8_pack_bytes(N, d), "pkH", X)
+    G = 0 if gate is None else gate.shape[0]
+    _check(_block_lib().stage_norm_pack(
+        _ptr(X, "X", dev), _ptr(Y, "Y", dev, dt, shape), _ptr(w_post, "w_post", dev, dt, (d,)),
+        _ptr(gate, "gate", dev, dt, (G, d)), _ptr(w_pre, "w_pre", dev, dt, (d,)),
+        _ptr(X_out, "X_out", dev, dt, shape), _ptr(H, "H", dev, dt, shape), pk_ptr, pk_size, float(res_scale),
+        float(eps), float(p), _u(seed, "seed"), _u(offset, "offset"), N, d, G, _dt(X), _raw_stream(dev)),
+        "stage_norm_pack")
+    return X_out, H, pkH
 
 
 # --------------------------------------------------------------- attention --
@@ -141,3 +177,65 @@ def stage_attn_bwd(gO, Q, K, V, O, lse, cu, scale=None, gQ=None, gK=None, gV=Non
         D ** -0.5 if scale is None else float(scale), cu.numel() - 1, N, Hq, Hkv, D, ldgo, ldq, ldk, ldv, ldo, ldgq,
         ldgk, ldgv, _dt(Q), ws_ptr, ws_size, _raw_stream(dev)), "stage_attn_bwd")
     return gQ, gK, gV
+
+
+# -------------------------------------------------------------------- loss --
+
+@functools.lru_cache(maxsize=4096)
+def stage_distill_workspace_bytes(N: int, V: int) -> int:
+    """Workspace of stage_distill for these sizes (0 where rows are not split)."""
+    return int(_block_lib().stage_distill_workspace_bytes(N, V))
+
+
+def _teacher(Z, labels, t_ids, t_logits, N, dev):
+    """Pointers of the labels and the teacher's entries, and K."""
+    if (t_ids is None) != (t_logits is None):
+        raise MaplError(-1, "binding", "t_ids and t_logits come together")
+    K = 0 if t_ids is None else t_ids.shape[-1]
+    lead = Z.shape[:-1]
+    return (_ptr(labels, "labels", dev, torch.int32, lead), _ptr(t_ids, "t_ids", dev, torch.int32, (*lead, K)),
+            _ptr(t_logits, "t_logits", dev, torch.float32, (*lead, K)), K)
+
+
+def stage_distill(Z, labels=None, t_ids=None, t_logits=None, temperature=1.0, w_ce=1.0, w_kd=1.0, loss=None, stats=None,
+                  ws=None, stream=None):
+    """Loss of logits Z [..., V]: w_ce times the cross-entropy with labels [...]
+    (int32, -1: none) plus w_kd times the divergence from the teacher's top logits
+    t_logits [..., K] (fp32) at t_ids [..., K] (int32, -1: no entry), at the
+    temperature.  Returns (loss [...], stats [..., 2]), fp32; stats is for
+    stage_distill_bwd."""
+    if _elsewhere(Z, "Z", stream):
+        with _there(Z, stream):
+            return stage_distill(Z, labels, t_ids, t_logits, temperature, w_ce, w_kd, loss, stats, ws)
+    N, V = _rows(Z, "Z")
+    dev, lead = Z.get_device(), Z.shape[:-1]
+    if loss is None:
+        loss = torch.empty(lead, dtype=torch.float32, device=Z.device)
+    if stats is None:
+        stats = torch.empty((*lead, 2), dtype=torch.float32, device=Z.device)
+    y, ids, logits, K = _teacher(Z, labels, t_ids, t_logits, N, dev)
+    ws, ws_ptr, ws_size = _bytes(ws, stage_distill_workspace_bytes(N, V), "ws", Z)
+    _check(_block_lib().stage_distill(
+        _ptr(Z, "Z", dev), y, ids, logits, _ptr(loss, "loss", dev, torch.float32, lead),
+        _ptr(stats, "stats", dev, torch.float32, (*lead, 2)), float(temperature), float(w_ce), float(w_kd), N, V, K,
+        _dt(Z), ws_ptr, ws_size, _raw_stream(dev)), "stage_distill")
+    return loss, stats
+
+
+def stage_distill_bwd(gloss, Z, stats, labels=None, t_ids=None, t_logits=None, temperature=1.0, w_ce=1.0, w_kd=1.0,
+                      gZ=None, stream=None):
+    """Gradient of stage_distill with respect to Z, given gloss [...] (fp32) and
+    the forward call's stats and arguments.  gZ may be Z."""
+    if _elsewhere(Z, "Z", stream):
+        with _there(Z, stream):
+            return stage_distill_bwd(gloss, Z, stats, labels, t_ids, t_logits, temperature, w_ce, w_kd, gZ)
+    N, V = _rows(Z, "Z")
+    dev, lead = Z.get_device(), Z.shape[:-1]
+    if gZ is None:
+        gZ = torch.empty_like(Z)
+    y, ids, logits, K = _teacher(Z, labels, t_ids, t_logits, N, dev)
+    _check(_block_lib().stage_distill_bwd(
+        _ptr(gloss, "gloss", dev, torch.float32, lead), _ptr(Z, "Z", dev),
+        _ptr(stats, "stats", dev, torch.float32, (*lead, 2)), y, ids, logits, _ptr(gZ, "gZ", dev, Z.dtype, Z.shape),
+        float(temperature), float(w_ce), float(w_kd), N, V, K, _dt(Z), _raw_stream(dev)), "stage_distill_bwd")
+    return gZ

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libmapl.so")
 ARCH = "gfx950"
 
 SOURCES = ["abi.hip", "pack.hip", "codec_bf16.hip", "codec_gemm.hip", "codec_f32.hip", "rvq.hip", "spel.hip", "anchor_grad.hip",
-           "stage.hip", "fp8.hip", "stage_abi.hip", "attn.hip", "block_abi.hip"]
+           "stage.hip", "fp8.hip", "stage_abi.hip", "attn.hip", "distill.hip", "block_abi.hip"]
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 VALU ops.
 COMMON_FLAGS = [

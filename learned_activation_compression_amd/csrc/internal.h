@@ -171,7 +171,9 @@ size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 void launch_fp8_gemm(const uint8_t* A, const uint8_t* B, void* C, int accumulate, int64_t M, int64_t N, int64_t K,
                      int bf16, float* ws, hipStream_t s);
 
-// ---- operators between a stage's edge and its loss (include/mapl_block.h)
+// ---- operators between a stage's boundary and its loss (include/mapl_block.h)
+void launch_stage_norm_pack(const StageNorm& c, uint8_t* pk, int bf16, hipStream_t s);
+
 struct Attn {  // leading dimensions in elements; the forward call leaves the gradients unset, the backward `out`
   const void *Q, *K, *V, *O, *gO;
   void *out, *gQ, *gK, *gV;
@@ -184,5 +186,18 @@ struct Attn {  // leading dimensions in elements; the forward call leaves the gr
 void launch_attn(const Attn& c, int bf16, hipStream_t s);
 size_t attn_bwd_ws_bytes(int64_t N, int64_t Hq, int64_t Hkv, int64_t D);
 void launch_attn_bwd(const Attn& c, int bf16, hipStream_t s);
+
+struct Distill {  // the forward call leaves gloss and gZ unset
+  const void* Z;
+  const int32_t *labels, *t_ids;
+  const float *t_logits, *gloss;
+  float *loss, *stats;
+  void* gZ;
+  float temperature, w_ce, w_kd;
+  int64_t N, V, K;
+};
+size_t distill_ws_bytes(int64_t N, int64_t V);
+void launch_distill(const Distill& c, int bf16, float* ws, hipStream_t s);
+void launch_distill_bwd(const Distill& c, int bf16, hipStream_t s);
 
 }  // namespace mapl

@@ -5,6 +5,7 @@
 // their sums and their use.
 #include <type_traits>
 
+#include "e4m3.h"
 #include "internal.h"
 #include "vec8.h"
 
@@ -167,13 +168,29 @@ struct NormArgs {
   Drop dr;
   int64_t N, rows_per_gate;
   int d;
+  View pk;  // of H
 };
+
+// Largest of 16 neighbouring lanes, the same in each of them
+__device__ __forceinline__ float lane_max16(float v) {
+  const auto dpp = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0xB1>{}));
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x4E>{}));
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x141>{}));
+  return fmaxf(v, dpp(v, std::integral_constant<int, 0x140>{}));
+}
 
 // Bound by its traffic, two tensors in and two out: 16384 x 1024 bf16 out of memory
 // in 25.8 us (5.2 TB/s) without and 28 us (4.8 TB/s) with dropout, whose generator
 // does not quite hide; 8192 x 2048 in 28.4 us.  All loads of a row, weights included,
 // are issued before the first sum; the weights come from the caches.
-template <typename T, int TPR, int V, RowMode MODE>
+//
+// PACK: H also leaves as an 8-bit operand.  A thread's 8 columns are a sixteenth of a
+// block of 128, so that a block's largest magnitude is found among 16 neighbouring
+// lanes, and its codes are half of a row's 16-byte piece.
+template <typename T, int TPR, int V, RowMode MODE, bool PACK>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
   __shared__ float lds[2 * 3 * 16];
@@ -202,7 +219,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) fg[j].issue(g, col(j), a.d);
     }
-    if (a.H) {
+    if (PACK || a.H) {
 #pragma unroll
       for (int j = 0; j < V; ++j) fw[j].issue(a.w_pre, col(j), a.d);
     }
@@ -256,7 +273,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) put_row<MODE>(a.X_out + at, col(j), a.d, in, x[j]);
     }
-    if (a.H) {
+    if (PACK || a.H) {
       float s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -269,7 +286,22 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
         const Raw8<T> w = fw[j].value(col(j), a.d, true);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[j][i] *= r * w.get(i);
-        put_row<MODE>(a.H + at, col(j), a.d, in, x[j]);
+        if (!PACK || a.H) put_row<MODE>(a.H + at, col(j), a.d, in, x[j]);
+        if constexpr (PACK) {
+          if (col(j) + 8 > a.d) {  // a row that is NaN leaves its padding zero
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[j][i] = col(j) + i < a.d ? x[j][i] : 0.f;
+          }
+          bool bad;
+          const float top = lane_max16(abs_max<8>(x[j], bad));
+          const int e = block_exp(top);
+          const int64_t kb = col(j) >> 7, rt = n >> 5;
+          if (in && kb < a.pk.KB) {
+            uint8_t* unit = a.pk.code + (rt * a.pk.KB + kb) * 4096 + unit_off(int(n & 31), (col(j) >> 4) & 7);
+            *reinterpret_cast<u32x2*>(unit + (col(j) & 8)) = codes8(x[j], pow2_neg(e), bad);
+            if ((l & 15) == 0) a.pk.exp[kb * a.pk.exp_stride + n] = static_cast<uint8_t>(e);
+          }
+        }
       }
     }
   }
@@ -604,14 +636,18 @@ void by_shape(SlotShape sh, const A& args, dim3 grid, hipStream_t s) {
   }
   return L<T, 512, 1>::go(args, grid, s);
 }
-template <typename T, int TPR, int V>
-struct FwdLaunch {
+template <typename T, int TPR, int V, bool PACK>
+struct FwdForm {
   static void go(const NormArgs<T>& a, dim3 grid, hipStream_t s) {
     by_row_mode<T, TPR == 16>(a.d, {a.X, a.Y, a.w_post, a.gate, a.w_pre, a.X_out, a.H}, [&](auto m) {
-      hipLaunchKernelGGL((k_stage_norm<T, TPR, V, decltype(m)::value>), grid, dim3(kBlock<TPR>), 0, s, a);
+      hipLaunchKernelGGL((k_stage_norm<T, TPR, V, decltype(m)::value, PACK>), grid, dim3(kBlock<TPR>), 0, s, a);
     });
   }
 };
+template <typename T, int TPR, int V>
+using FwdLaunch = FwdForm<T, TPR, V, false>;
+template <typename T, int TPR, int V>
+using PackLaunch = FwdForm<T, TPR, V, true>;
 template <typename T, int TPR, int V>
 struct BwdLaunch {
   template <bool PRE, bool POST, bool MANY>
@@ -645,8 +681,8 @@ void launch_dropout(const void* X, void* Y, double p, uint64_t seed, uint64_t of
   (bf16 ? dropout_t<bf16_t> : dropout_t<float>)(X, Y, p, seed, offset, N, d, s);
 }
 
-template <typename T>
-static void norm_t(const StageNorm& c, hipStream_t s) {
+template <typename T, bool PACK>
+static void norm_t(const StageNorm& c, const uint8_t* pk, hipStream_t s) {
   NormArgs<T> a;
   a.X = static_cast<const T*>(c.X);
   a.Y = static_cast<const T*>(c.Y);
@@ -665,10 +701,20 @@ static void norm_t(const StageNorm& c, hipStream_t s) {
   const SlotShape sh = slot_shape(c.d, false);
   const int64_t S = slots_per_block(sh);
   const uint32_t grid = uint32_t(std::min<int64_t>((c.N + S - 1) / S, 256 * 8));
-  by_shape<T, FwdLaunch, false>(sh, a, dim3(grid), s);
+  if constexpr (PACK) {
+    a.pk = View(pk, c.N, c.d);
+    by_shape<T, PackLaunch, false>(sh, a, dim3(grid), s);
+  } else {
+    by_shape<T, FwdLaunch, false>(sh, a, dim3(grid), s);
+  }
 }
 
-void launch_stage_norm(const StageNorm& c, int bf16, hipStream_t s) { (bf16 ? norm_t<bf16_t> : norm_t<float>)(c, s); }
+void launch_stage_norm(const StageNorm& c, int bf16, hipStream_t s) {
+  (bf16 ? norm_t<bf16_t, false> : norm_t<float, false>)(c, nullptr, s);
+}
+void launch_stage_norm_pack(const StageNorm& c, uint8_t* pk, int bf16, hipStream_t s) {
+  (bf16 ? norm_t<bf16_t, true> : norm_t<float, true>)(c, pk, s);
+}
 
 size_t stage_norm_bwd_ws_bytes(int64_t N, int64_t d, int64_t gate_rows) {
   return size_t(3) * bwd_split(N, d, gate_rows).blocks * d * sizeof(float);

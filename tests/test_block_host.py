@@ -124,3 +124,118 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(lac.MaplError) as e:
             call()
         assert e.value.status == -1
+
+
+# -------------------------------------------------------------------- loss --
+
+@pytest.mark.parametrize("T, w_ce, w_kd", [(1.0, 1.0, 0.0), (2.0, 0.3, 4.0), (1.0, 0.0, 1.0), (0.5, 1.0, 1.0)])
+def test_loss_gradient_against_differences(T, w_ce, w_kd):
+    rng = np.random.default_rng(7)
+    N, V, K = 5, 9, 4
+    Z, t, g = rng.standard_normal((N, V)), rng.standard_normal((N, K)), rng.standard_normal(N)
+    y, ids = np.array([0, -1, 8, 3, 9]), rng.integers(0, V, (N, K))
+    ids[1], ids[2, 1], ids[3] = -1, 40, [2, 2, 3, 2]  # a row of none, an id too large, one id three times
+    t[0, 0] = -np.inf
+    got, _ = block.distill_bwd(g, Z, y, ids, t, T, w_ce, w_kd)
+    num = differences(lambda Z: np.sum(g * block.distill(Z, y, ids, t, T, w_ce, w_kd)[0]), dict(Z=Z), "Z")
+    np.testing.assert_allclose(got, num, rtol=1e-6, atol=1e-6)
+    assert np.all(got[1] == 0)
+
+
+def test_loss_of_equal_logits_and_of_the_teacher_itself():
+    Z, ids = np.zeros((2, 8)), np.array([[0, 1], [5, 6]])
+    loss, stats, _ = block.distill(Z, np.array([3, -1]), ids, np.zeros((2, 2)), 1.0, 1.0, 0.0)
+    assert np.allclose(loss, [np.log(8), 0]) and np.allclose(stats, np.log(8))
+    # a teacher that gives all entries and agrees: no divergence and no gradient
+    Z = np.random.default_rng(0).standard_normal((1, 8))
+    args = (None, np.arange(8)[None], Z.copy(), 2.0, 1.0, 1.0)
+    assert np.allclose(block.distill(Z, *args)[0], 0) and np.allclose(block.distill_bwd(np.ones(1), Z, *args)[0], 0)
+
+
+def _distill(lib, **kw):
+    a = dict(Z=FAKE, labels=FAKE, t_ids=FAKE, t_logits=FAKE, loss=FAKE, stats=FAKE, T=2.0, w_ce=1.0, w_kd=1.0, N=0, V=100,
+             K=8, dt=BF16, ws=FAKE, ws_bytes=1 << 40)
+    a.update(kw)
+    return lib.stage_distill(*a.values(), None)
+
+
+def _distill_bwd(lib, **kw):
+    a = dict(gloss=FAKE, Z=FAKE, stats=FAKE, labels=FAKE, t_ids=FAKE, t_logits=FAKE, gZ=FAKE, T=2.0, w_ce=1.0, w_kd=1.0,
+             N=0, V=100, K=8, dt=BF16)
+    a.update(kw)
+    return lib.stage_distill_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [_distill, _distill_bwd])
+def test_loss_refusals(lib, call):
+    assert call(lib) == OK and call(lib, Z=None, stats=None) == OK  # no rows
+    assert call(lib, dt=2) == EDTYPE
+    for bad in (dict(N=-1), dict(N=2 ** 23 + 1), dict(V=0), dict(V=2 ** 27 + 1), dict(K=-1), dict(K=1025),
+                dict(N=2 ** 20, V=2 ** 17)):
+        assert call(lib, **bad) == ESHAPE, bad
+    for bad in (dict(T=0.0), dict(T=-1.0), dict(T=float("inf")), dict(T=float("nan")), dict(T=1e-40),
+                dict(w_ce=float("nan")), dict(w_kd=float("inf"))):
+        assert call(lib, **bad) == EARG, bad
+    for n in ("Z", "stats", "t_ids", "t_logits"):
+        assert call(lib, N=4, **{n: None}) == ENULL, n
+        assert call(lib, N=4, **{n: ODD}) == EARG, n
+    assert call(lib, N=4, labels=ODD) == EARG
+
+
+def test_loss_refusals_of_one_direction(lib):
+    assert _distill(lib, N=4, loss=None) == ENULL and _distill(lib, N=4, loss=ODD) == EARG
+    for n in ("gloss", "gZ"):
+        assert _distill_bwd(lib, N=4, **{n: None}) == ENULL and _distill_bwd(lib, N=4, **{n: ODD}) == EARG
+    need = lib.stage_distill_workspace_bytes(4, 32000)
+    assert need > 0 and lib.stage_distill_workspace_bytes(4, 100) == 0 and lib.stage_distill_workspace_bytes(5000, 32000) == 0
+    assert lib.stage_distill_workspace_bytes(0, 100) == 0 and lib.stage_distill_workspace_bytes(4, -1) == 0
+    big = dict(N=4, V=32000)
+    assert _distill(lib, **big, ws=None) == ENULL and _distill(lib, **big, ws=ctypes.c_void_p(0x1008)) == EARG
+    assert _distill(lib, **big, ws_bytes=need - 1) == EWS
+
+
+@no_device
+@pytest.mark.parametrize("call", [_distill, _distill_bwd])
+def test_loss_takes_what_it_documents(lib, call):
+    for kw in (dict(N=1), dict(N=2 ** 23, V=1), dict(N=1, V=2 ** 27), dict(N=3, K=0, t_ids=None, t_logits=None),
+               dict(N=3, labels=None), dict(N=3, K=1024), dict(N=3, dt=F32)):
+        assert call(lib, **kw) == EHIP, kw
+
+
+# -------------------------------------------------------------- block edge --
+
+def _norm_pack(lib, **kw):
+    a = dict(X=FAKE, Y=FAKE, w_post=FAKE, gate=FAKE, w_pre=FAKE, X_out=FAKE, H=FAKE, pk=FAKE, pk_bytes=1 << 40,
+             res_scale=1.0, eps=1e-5, p=0.1, seed=1, offset=0, N=0, d=64, G=1, dt=BF16)
+    a.update(kw)
+    return lib.stage_norm_pack(*a.values(), None)
+
+
+def test_norm_pack_refusals(lib):
+    assert _norm_pack(lib) == OK and _norm_pack(lib, X=None, pk=None) == OK
+    assert _norm_pack(lib, dt=9) == EDTYPE
+    for bad in (dict(N=-1), dict(N=2 ** 27 + 1), dict(N=2 ** 24, d=8192), dict(d=0), dict(d=8193), dict(G=-1),
+                dict(N=10, G=3), dict(N=2, G=4)):
+        assert _norm_pack(lib, **bad) == ESHAPE, bad
+    for bad in (dict(eps=0.0), dict(eps=float("nan")), dict(p=1.5), dict(res_scale=float("inf")), dict(gate=None), dict(G=0),
+                dict(N=4, Y=None), dict(N=4, X=ODD), dict(N=4, H=ODD), dict(N=4, pk=ctypes.c_void_p(0x1008))):
+        assert _norm_pack(lib, **bad) == EARG, bad
+    for n in ("X", "w_pre", "pk"):
+        assert _norm_pack(lib, N=4, **{n: None}) == ENULL, n
+    assert _norm_pack(lib, N=4, pk_bytes=lib.fp8_pack_bytes(4, 64) - 1) == EWS
+
+
+@no_device
+def test_norm_pack_takes_what_it_documents(lib):
+    none = dict(Y=None, p=0.0, w_post=None, gate=None, G=0)
+    for kw in (dict(N=4), dict(N=4, X_out=None, H=None), dict(N=4, **none), dict(N=2 ** 23, d=8192), dict(N=5, d=7, dt=F32)):
+        assert _norm_pack(lib, **kw) == EHIP, kw
+
+
+def test_binding_refuses_host_tensors_of_the_other_operators():
+    x = torch.zeros(4, 8)
+    for call in (lambda: lac.stage_norm_pack(x, w_pre=x[0]), lambda: lac.stage_distill(x),
+                 lambda: lac.stage_distill_bwd(x[:, 0], x, x[:, :2])):
+        with pytest.raises(lac.MaplError) as e:
+            call()
+        assert e.value.status == -1
