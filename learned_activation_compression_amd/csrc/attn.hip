@@ -65,8 +65,8 @@ __device__ __forceinline__ f32x16 mma(Operand<float> a, Operand<float> b, f32x16
 template <typename T>
 __device__ __forceinline__ Operand<T> as_operand(const f32x16& x, int u) {
   if constexpr (sizeof(T) == 2) {
-    return {__builtin_bit_cast(bf16x8, u32x4{pack2bf(x[8 * u], x[8 * u + 1]), pack2bf(x[8 * u + 2], x[8 * u + 3]),
-                                             pack2bf(x[8 * u + 4], x[8 * u + 5]), pack2bf(x[8 * u + 6], x[8 * u + 7])})};
+    return {__builtin_bit_cast(bf16x8, u32x4{cvt2bf(x[8 * u], x[8 * u + 1]), cvt2bf(x[8 * u + 2], x[8 * u + 3]),
+                                             cvt2bf(x[8 * u + 4], x[8 * u + 5]), cvt2bf(x[8 * u + 6], x[8 * u + 7])})};
   } else {
     Operand<float> o;
 #pragma unroll
@@ -110,47 +110,19 @@ __device__ __forceinline__ Operand<T> load_row(const T* row, int c, int D) {
 // the permutation.  It keeps apart in the banks
 //   - 8 consecutive rows at one column (operands by rows, 16 bytes a lane);
 //   - bf16: 4 rows at 16 columns (reads that transpose, 8 bytes a lane);
-//   - fp32: rows r and r + 4 at 32 columns (operands by columns).
+//   - fp32: rows r and r + 4 at 32 columns (operands by columns);
+// measured in a loop of such reads on every SIMD: 4.2 cycles for 16 bytes a lane, 2.6 for
+// 8 and for 4, as without any permutation in contiguous reads.
 template <typename T, int DP>
 struct Tile {
   static constexpr int E = 16 / sizeof(T);                               // elements of a chunk
   static constexpr int kSlots = DP <= 64 ? 64 / E : 128 / E;             // a power of two
   static constexpr int kRowBytes = kSlots * 16;
   static __device__ __forceinline__ int turn(int r) {
-    if constexpr (sizeof(T) == 4) return ((r & 3) << 1) | ((r & 4) << 1) | ((r >> 3) & 1);
-    if constexpr (kSlots == 8) return (r & 6) | ((r >> 3) & 1);
-    return ((r & 7) << 1) | ((r >> 3) & 1);
+    if constexpr (kSlots == 8) return ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
+    return ((r & 3) << 2) | ((r >> 2) & 3);
   }
   static __device__ __forceinline__ int at(int r, int c) { return r * kRowBytes + ((c ^ turn(r)) << 4); }
-
-  // the wave's share of rows r0 .. r0 + ROWS - 1, clamped to [0, N)
-  template <int ROWS, int WAVES, bool ALIGNED>
-  static __device__ __forceinline__ void stage(char* lds, const T* base, int64_t ld, int r0, int N, int D) {
-    constexpr int PER = ROWS * kSlots / 64 / WAVES;
-    static_assert(ROWS * kSlots % (64 * WAVES) == 0, "whole copies");
-    const int lane = threadIdx.x & 63, w = wave_id();
-    const int chunks = (D + E - 1) / E;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int unit = w + k * WAVES, slot = unit * 64 + lane, r = slot / kSlots;
-      const int c = (slot % kSlots) ^ turn(r);
-      const T* row = base + int64_t(min(max(r0 + r, 0), N - 1)) * ld;
-      if constexpr (ALIGNED) {
-        copy16_to_lds(row + (c < chunks ? c * E : 0), lds + unit * 1024);
-      } else {
-        u32x4 v;
-        if constexpr (sizeof(T) == 2) {
-          Raw8<T> x;
-          load8(x, row + (c < chunks ? c * E : 0), c < chunks ? min(8, D - c * E) : 0);
-          v = x.a;
-        } else {
-          const int left = c < chunks ? D - c * E : 0;
-          v = left >= 4 ? ld16B(row + c * E) : ld_tail4(row + (left > 0 ? c * E : 0), left);
-        }
-        *reinterpret_cast<u32x4*>(lds + slot * 16) = v;
-      }
-    }
-  }
 
   // rows r0 + (l & 31), columns 16 t + 8 h .. + 7
   static __device__ __forceinline__ Operand<T> by_rows(const char* lds, int r0, int t) {
@@ -186,6 +158,61 @@ struct Tile {
   }
 };
 
+// The copies of a tile's rows to LDS, a wave's share of them: lane offsets once, the
+// tile's place in a uniform base.  Rows behind the last are read at the last.
+template <typename T, int DP, int ROWS, int WAVES, bool ALIGNED>
+struct Stager {
+  using L = Tile<T, DP>;
+  static constexpr int PER = ROWS * L::kSlots / 64 / WAVES;
+  static_assert(PER > 0 && ROWS * L::kSlots % (64 * WAVES) == 0, "whole copies");
+  uint32_t ld;  // bytes of a row
+  int D;
+  uint32_t off[PER];
+
+  static __device__ __forceinline__ int slot(int k) { return (wave_id() + k * WAVES) * 64 + (threadIdx.x & 63); }
+  __device__ __forceinline__ uint32_t chunk(int k) const {  // byte offset within a row
+    const int c = (slot(k) % L::kSlots) ^ L::turn(slot(k) / L::kSlots);
+    return c * L::E < D ? c * 16 : 0;
+  }
+  __device__ __forceinline__ Stager(int64_t ld_elems, int D_) : ld(uint32_t(ld_elems) * sizeof(T)), D(D_) {
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int k = 0; k < PER; ++k) off[k] = uint32_t(slot(k) / L::kSlots) * ld + chunk(k);
+    }
+  }
+  // rows r0 .. of the tensor's rows at `base` to the tile `lds`
+  __device__ __forceinline__ void operator()(char* lds, const T* base, int r0, int N) const {
+    const char* at = reinterpret_cast<const char*>(base) + int64_t(r0) * ld;
+    if constexpr (ALIGNED) {
+      const uint32_t to = lds_address(lds) + wave_id() * 1024;
+      if (r0 + ROWS <= N) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) copy_lane16_to_lds(at, off[k], to + k * WAVES * 1024);
+      } else {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+          copy_lane16_to_lds(at, uint32_t(min(slot(k) / L::kSlots, N - 1 - r0)) * ld + chunk(k), to + k * WAVES * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int r = slot(k) / L::kSlots, c = (slot(k) % L::kSlots) ^ L::turn(r);
+        const T* row = reinterpret_cast<const T*>(at + int64_t(min(r, N - 1 - r0)) * ld);
+        const int left = max(0, D - c * L::E);
+        u32x4 v;
+        if constexpr (sizeof(T) == 2) {
+          Raw8<T> x;
+          load8(x, row + (left > 0 ? c * L::E : 0), min(8, left));
+          v = x.a;
+        } else {
+          v = left >= 4 ? ld16B(row + c * L::E) : ld_tail4(row + (left > 0 ? c * L::E : 0), left);
+        }
+        *reinterpret_cast<u32x4*>(lds + slot(k) * 16) = v;
+      }
+    }
+  }
+};
+
 // both half-waves' values of a column joined
 template <typename F>
 __device__ __forceinline__ float join_halves(float v, F f) {
@@ -199,12 +226,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s);
   return v;
-}
-
-// as copy16_to_lds, 4 bytes a lane
-__device__ __forceinline__ void copy4_to_lds(const void* g, const void* l_base) {
-  const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(l_base)));
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(g), "s"(la) : "memory", "m0");
 }
 
 // ----------------------------------------------------------------- sequences --
@@ -243,7 +264,9 @@ struct AttnArgs {
   const T *Q, *K, *V, *O, *gO;
   T *out, *gQ, *gK, *gV;
   const int32_t* cu;
-  float *lse, *rows;  // lse [Hq][N]; rows [2][Hq][N]: lse in units of log 2, then delta
+  float *lse, *rows;  // lse [Hq][N]; rows [Hq][2][N]: lse in units of log 2, and delta
+  float* part;        // sums of a split: gQ [splits][N][Hq D]; gK, gV [splits][N][2][Hkv D]
+  int splits;
   int64_t ldq, ldk, ldv, ldo, ldgo, ldgq, ldgk, ldgv;
   float scale;
   int S, N, Hq, Hkv, D;
@@ -255,7 +278,7 @@ __device__ __forceinline__ void put4(T* row, int c, int D, float a, float b, flo
   if (c >= D) return;
   if constexpr (ALIGNED) {
     if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<u32x2*>(row + c) = u32x2{pack2bf(a, b), pack2bf(x, y)};
+      *reinterpret_cast<u32x2*>(row + c) = u32x2{cvt2bf(a, b), cvt2bf(x, y)};
     else
       *reinterpret_cast<f32x4*>(row + c) = f32x4{a, b, x, y};
   } else {
@@ -322,8 +345,8 @@ __device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int
   if ((threadIdx.x & 63) == 0) a.lse[int64_t(h) * a.N + i] = m + logf(l);
 }
 
-template <typename T, int DP, int QB, int WAVES, int BN, bool ALIGNED>
-__global__ __launch_bounds__(64 * WAVES) void k_attn_fwd(AttnArgs<T> a) {
+template <typename T, int DP, int QB, int WAVES, int BN, int OCC, bool ALIGNED>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   using L = Tile<T, DP>;
   constexpr int NT = DP / 16, NB = DP / 32, KB = BN / 32, BM = 32 * QB * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -343,11 +366,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd(AttnArgs<T> a) {
   const int kmin = __builtin_amdgcn_readfirstlane(find_seq(cu, a.S, i0, a.N).start);
   const int kmax = min(i0 + BM, a.N);  // behind the last key
   const int turns = (kmax - kmin + BN - 1) / BN;
-  const auto stage = [&](int n) {
-    L::template stage<BN, WAVES, ALIGNED>(k_tile(n & 1), Kb, a.ldk, kmin + n * BN, a.N, a.D);
-    L::template stage<BN, WAVES, ALIGNED>(v_tile(n & 1), Vb, a.ldv, kmin + n * BN, a.N, a.D);
-  };
-  stage(0);
+  const Stager<T, DP, BN, WAVES, ALIGNED> stage_k(a.ldk, a.D), stage_v(a.ldv, a.D);
+  stage_k(k_tile(0), Kb, kmin, a.N);
 
   Operand<T> q[QB][NT];
   Seq seq[QB];
@@ -359,9 +379,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd(AttnArgs<T> a) {
 #pragma unroll
     for (int s = 0; s < NT; ++s) q[b][s] = load_row<T, ALIGNED>(row, 16 * s + 8 * hi, a.D);
   }
-  // the wave's keys: from its first row's start to its last row; all of them see a tile
-  // that begins at or behind the last row's start and ends at or before the first row
-  const int first = __builtin_amdgcn_readfirstlane(seq[0].start);
+  // the wave's tiles nb .. ne - 1, from its first row's start to its last row; all of its
+  // rows see a tile that begins at or behind the last row's start and ends at or before
+  // the first row
+  const int nb = (max(__builtin_amdgcn_readfirstlane(seq[0].start), kmin) - kmin) / BN;
+  const int ne = min((w0 + 32 * QB - kmin + BN - 1) / BN, turns);
   const int lastStart = __builtin_amdgcn_readlane(seq[QB - 1].start, 31);
 
   f32x16 o[QB][NB];
@@ -375,71 +397,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd(AttnArgs<T> a) {
   }
   const float c = a.scale * kLog2e, slack = 8.f / c;
 
-  for (int n = 0; n < turns; ++n) {
-    wait_vmcnt<0>();
-    __syncthreads();
-    if (n + 1 < turns) stage(n + 1);
-    const int k0 = kmin + n * BN;
-    if (k0 + BN <= first || k0 >= w0 + 32 * QB) continue;
-    const bool whole = k0 + BN - 1 <= w0 && k0 >= lastStart;
-    const char *kt = k_tile(n & 1), *vt = v_tile(n & 1);
-    f32x16 s[QB][KB];
+  f32x16 s[QB][KB];        // scores of a tile, then its weights
+  Operand<T> p[QB][KB][2];  // the weights as operands
+  float mc[QB];
+  const auto scores = [&](int x, const char* kt) {
 #pragma unroll
-    for (int x = 0; x < KB; ++x) {
+    for (int b = 0; b < QB; ++b) s[b][x] = zero16();
 #pragma unroll
-      for (int b = 0; b < QB; ++b) s[b][x] = zero16();
+    for (int u = 0; u < NT; ++u) {
+      const Operand<T> k = L::by_rows(kt, 32 * x, u);
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        const Operand<T> k = L::by_rows(kt, 32 * x, u);
-#pragma unroll
-        for (int b = 0; b < QB; ++b) s[b][x] = mma(k, q[b][u], s[b][x]);
-      }
+      for (int b = 0; b < QB; ++b) s[b][x] = mma(k, q[b][u], s[b][x]);
     }
-    Operand<T> p[QB][KB][2];
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      if (!whole) {
-        const int i = w0 + 32 * b + col;
-#pragma unroll
-        for (int x = 0; x < KB; ++x)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int j = k0 + 32 * x + mfma32_row(v, hi);
-            s[b][x][v] = j >= seq[b].start && j <= i ? s[b][x][v] : -INFINITY;
-          }
-      }
-      float top = s[b][0][0];
-#pragma unroll
-      for (int x = 0; x < KB; ++x)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) top = fmaxf(top, s[b][x][v]);
-      top = join_halves(top, max2);
-      // The reference stays until a score passes it by 2^8: weights up to 2^8 lose nothing
-      // in a float, and the sums are seldom scaled.
-      if (__any(top > m[b] + slack)) {
-        const float mn = top > m[b] + slack ? top : m[b];
-        const float f = m[b] == mn ? 1.f : __builtin_amdgcn_exp2f((m[b] - mn) * c);
-        m[b] = mn;
-        l[b] *= f;
-#pragma unroll
-        for (int d = 0; d < NB; ++d)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) o[b][d][v] *= f;
-      }
-      const float mc = m[b] == -INFINITY ? 0.f : m[b] * c;
-      float sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < KB; ++x) {
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          s[b][x][v] = __builtin_amdgcn_exp2f(fmaf(s[b][x][v], c, -mc));
-          sum += s[b][x][v];
-        }
-        p[b][x][0] = as_operand<T>(s[b][x], 0);
-        p[b][x][1] = as_operand<T>(s[b][x], 1);
-      }
-      l[b] += sum;
-    }
+  };
+  const auto values = [&](const char* vt) {
 #pragma unroll
     for (int x = 0; x < KB; ++x)
 #pragma unroll
@@ -450,7 +421,103 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd(AttnArgs<T> a) {
 #pragma unroll
           for (int b = 0; b < QB; ++b) o[b][d] = mma(v, p[b][x][u], o[b][d]);
         }
+  };
+  const auto mask = [&](int k0) {
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      // start <= j <= i in one comparison
+      const uint32_t most = w0 + 32 * b + col - seq[b].start, at = k0 + 4 * hi - seq[b].start;
+#pragma unroll
+      for (int x = 0; x < KB; ++x)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[b][x][v] = at + (32 * x + mfma32_row(v, 0)) <= most ? s[b][x][v] : -INFINITY;
+    }
+  };
+  // The reference m of a row's weights exp(s - m) stays until a score passes it by 2^8:
+  // weights up to 2^8 lose nothing in a float, and the sums are seldom scaled (by f).
+  const auto reference = [&](float (&f)[QB]) {
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      float top = s[b][0][0];
+#pragma unroll
+      for (int x = 0; x < KB; ++x)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) top = fmaxf(top, s[b][x][v]);
+      top = join_halves(top, max2);
+      const float mn = top > m[b] + slack ? top : m[b];
+      f[b] = m[b] == mn ? 1.f : __builtin_amdgcn_exp2f((m[b] - mn) * c);
+      l[b] *= f[b];
+      m[b] = mn;
+      mc[b] = mn == -INFINITY ? 0.f : mn * c;
+    }
+  };
+  const auto weights = [&](int x) {
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[b][x][v] = __builtin_amdgcn_exp2f(fmaf(s[b][x][v], c, -mc[b]));
+        sum[v & 1] += s[b][x][v];
+      }
+      l[b] += sum[0] + sum[1];
+    }
+  };
+  const auto operands = [&](int x) {
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      p[b][x][0] = as_operand<T>(s[b][x], 0);
+      p[b][x][1] = as_operand<T>(s[b][x], 1);
+    }
+  };
+  const auto begin = [&](int n) {  // a turn's wait and copies
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (n + 2 < turns) stage_k(k_tile(n & 1), Kb, kmin + (n + 2) * BN, a.N);
+    if (n >= 0 && n < turns) stage_v(v_tile(n & 1), Vb, kmin + n * BN, a.N);
+  };
+  // Turn n: the values of tile n - 1, the softmax of tile n and the scores of tile n + 1,
+  // which are independent of each other, so that the matrix and the vector units work
+  // at a time.
+  int n = -1;
+  for (; n < nb - 1; ++n) begin(n);
+  begin(n);
+#pragma unroll
+  for (int x = 0; x < KB; ++x) scores(x, k_tile((n + 1) & 1));
+  for (n = nb; n < ne; ++n) {
+    begin(n);
+    const int k0 = kmin + n * BN;
+    if (!(k0 + BN - 1 <= w0 && k0 >= lastStart)) mask(k0);
+    float f[QB];
+    if (n > nb) {
+      const char* vt = v_tile((n + 1) & 1);
+      values(vt);
+      reference(f);
+      weights(0);
+    } else {
+      reference(f);
+      weights(0);
+    }
+#pragma unroll
+    for (int b = 0; b < QB; ++b)
+      if (__any(f[b] != 1.f)) {
+#pragma unroll
+        for (int d = 0; d < NB; ++d)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) o[b][d][v] *= f[b];
+      }
+    // behind the wave's last tile the next scores are of no use
+    const char* kt = k_tile((n + 1) & 1);
+#pragma unroll
+    for (int x = 0; x < KB; ++x) {
+      operands(x);
+      scores(x, kt);
+      if (x + 1 < KB) weights(x + 1);
+    }
   }
+  begin(n);
+  values(v_tile((n + 1) & 1));
+  for (++n; n <= turns; ++n) begin(n);
 
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
@@ -467,6 +534,131 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd(AttnArgs<T> a) {
       for (int r = 0; r < 32; ++r)
         if (__builtin_amdgcn_readlane(int(in), r)) fwd_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r));
     }
+  }
+}
+
+// Few rows: a block owns 32 query rows, and its waves take a part of every tile of
+// 32 WAVES keys each, with a softmax of their own; their sums are joined at the end.
+template <typename T, int DP, int WAVES, int BUFS, bool ALIGNED>
+__global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
+  using L = Tile<T, DP>;
+  constexpr int NT = DP / 16, NB = DP / 32, BN = 32 * WAVES;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  __shared__ int32_t cu_lds[kCuLds];
+  __shared__ float ms[WAVES][2][32];  // of each wave: reference and sum
+  constexpr int TILE = BN * L::kRowBytes;
+  const auto k_tile = [&](int n) { return smem + (n % BUFS) * 2 * TILE; };
+  const auto v_tile = [&](int n) { return smem + (n % BUFS) * 2 * TILE + TILE; };
+
+  const int t = (a.N + 31) / 32 - 1 - blockIdx.x / a.Hq;
+  const int h = xcd_swizzle(blockIdx.x % a.Hq, a.Hq), kv = h / (a.Hq / a.Hkv);
+  const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5, w = wave_id();
+  const int i0 = t * 32, i = i0 + col;
+  const int32_t* cu = edges(a.cu, a.S, cu_lds);
+  const T *Kb = a.K + int64_t(kv) * a.D, *Vb = a.V + int64_t(kv) * a.D;
+  const Seq seq = find_seq(cu, a.S, i, a.N);
+  const int kmin = __builtin_amdgcn_readfirstlane(seq.start);
+  const int turns = (min(i0 + 32, a.N) - kmin + BN - 1) / BN;
+  const Stager<T, DP, BN, WAVES, ALIGNED> stage_k(a.ldk, a.D), stage_v(a.ldv, a.D);
+  const auto stage = [&](int n) {
+    stage_k(k_tile(n), Kb, kmin + n * BN, a.N);
+    stage_v(v_tile(n), Vb, kmin + n * BN, a.N);
+  };
+  stage(0);
+  Operand<T> q[NT];
+  const T* qr = a.Q + int64_t(min(i, a.N - 1)) * a.ldq + int64_t(h) * a.D;
+#pragma unroll
+  for (int u = 0; u < NT; ++u) q[u] = load_row<T, ALIGNED>(qr, 16 * u + 8 * hi, a.D);
+  f32x16 o[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d) o[d] = zero16();
+  float m = -INFINITY, l = 0.f;
+  const float c = a.scale * kLog2e;
+  for (int n = 0; n < turns; ++n) {
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (BUFS > 1 && n + 1 < turns) stage(n + 1);
+    const int k0 = kmin + n * BN + 32 * w;
+    if (k0 < i0 + 32) {
+      const char *kt = k_tile(n), *vt = v_tile(n);
+      f32x16 s = zero16();
+#pragma unroll
+      for (int u = 0; u < NT; ++u) s = mma(L::by_rows(kt, 32 * w, u), q[u], s);
+      const uint32_t most = i - seq.start, at = k0 + 4 * hi - seq.start;
+      float top = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[v] = at + mfma32_row(v, 0) <= most ? s[v] : -INFINITY;
+        top = fmaxf(top, s[v]);
+      }
+      const float mn = fmaxf(m, join_halves(top, max2));
+      const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
+      const float mc = mn == -INFINITY ? 0.f : mn * c;
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], c, -mc));
+        l += s[v];
+      }
+#pragma unroll
+      for (int d = 0; d < NB; ++d) {
+        o[d] *= f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) o[d] = mma(L::by_cols(vt, 32 * w + 16 * u, d), as_operand<T>(s, u), o[d]);
+      }
+    }
+    if (BUFS == 1 && n + 1 < turns) {
+      __syncthreads();
+      stage(n + 1);
+    }
+  }
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);  // [WAVES][DP][32]
+  static_assert(WAVES * DP * 32 * 4 <= BUFS * 2 * TILE, "the tiles' room");
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) part[(w * DP + 32 * d + mfma32_row(v, hi)) * 32 + col] = o[d][v];
+  l = join_halves(l, sum2);
+  if (hi == 0) {
+    ms[w][0][col] = m;
+    ms[w][1][col] = l;
+  }
+  __syncthreads();
+  float f[WAVES], sum = 0.f;
+  m = ms[0][0][col];
+#pragma unroll
+  for (int x = 1; x < WAVES; ++x) m = fmaxf(m, ms[x][0][col]);
+#pragma unroll
+  for (int x = 0; x < WAVES; ++x) {
+    const float mx = ms[x][0][col];
+    f[x] = mx == m ? 1.f : __builtin_amdgcn_exp2f((mx - m) * c);
+    sum += f[x] * ms[x][1][col];
+  }
+  const float inv = 1.f / sum;
+  // a thread's columns: a 2 WAVES-th of its row
+  constexpr int PER = DP / (2 * WAVES);
+  static_assert(PER % 4 == 0, "whole stores");
+  const int c0 = (2 * w + hi) * PER;
+  T* row = a.out + int64_t(min(i, a.N - 1)) * a.ldo + int64_t(h) * a.D;
+  float bad = 0.f;
+#pragma unroll
+  for (int e = 0; e < PER; e += 4) {
+    float y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      y[k] = 0.f;
+#pragma unroll
+      for (int x = 0; x < WAVES; ++x) y[k] += f[x] * part[(x * DP + c0 + e + k) * 32 + col];
+      bad = c0 + e + k < a.D ? fmaf(0.f, y[k], bad) : bad;
+    }
+    if (seq.inside) put4<T, ALIGNED>(row, c0 + e, a.D, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+  }
+  if (seq.inside && hi == 0 && w == 0) a.lse[int64_t(h) * a.N + i] = (m * c + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (__syncthreads_or(seq.inside && (bad != bad || !(sum < INFINITY)))) {
+    for (int r = w; r < 32; r += WAVES)
+      if (__builtin_amdgcn_readlane(int(seq.inside), r)) fwd_row(a, h, kv, i0 + r, __builtin_amdgcn_readlane(seq.start, r));
   }
 }
 
@@ -487,8 +679,8 @@ __device__ __forceinline__ void dq_row(const AttnArgs<T>& a, int h, int kv, int 
   put_lanes(a.gQ + i * a.ldgq + hd, a.D, ga, gb);
 }
 
-template <typename T, int DP, int QB, int WAVES, int BN, bool ALIGNED>
-__global__ __launch_bounds__(64 * WAVES) void k_attn_dq(AttnArgs<T> a) {
+template <typename T, int DP, int QB, int WAVES, int BN, int OCC, bool ALIGNED>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
   using L = Tile<T, DP>;
   constexpr int NT = DP / 16, NB = DP / 32, KB = BN / 32, BM = 32 * QB * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -498,21 +690,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dq(AttnArgs<T> a) {
   const auto v_tile = [&](int b) { return smem + b * 2 * TILE + TILE; };
 
   const int tiles = (a.N + BM - 1) / BM;
-  const int t = tiles - 1 - blockIdx.x / a.Hq;
-  const int h = xcd_swizzle(blockIdx.x % a.Hq, a.Hq), kv = h / (a.Hq / a.Hkv);
+  const int heads = a.Hq * a.splits;
+  const int t = tiles - 1 - blockIdx.x / heads;
+  const int sp = blockIdx.x % heads / a.Hq, h = xcd_swizzle(blockIdx.x % a.Hq, a.Hq), kv = h / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
   const int i0 = t * BM, w0 = i0 + wave_id() * 32 * QB;
   const int32_t* cu = edges(a.cu, a.S, cu_lds);
   const T *Kb = a.K + int64_t(kv) * a.D, *Vb = a.V + int64_t(kv) * a.D;
 
-  const int kmin = __builtin_amdgcn_readfirstlane(find_seq(cu, a.S, i0, a.N).start);
+  // the split's tiles: sp, sp + splits, ... of the block's range
+  const int kmin = __builtin_amdgcn_readfirstlane(find_seq(cu, a.S, i0, a.N).start) + sp * BN, step = a.splits * BN;
   const int kmax = min(i0 + BM, a.N);
-  const int turns = (kmax - kmin + BN - 1) / BN;
+  const int turns = (kmax - kmin + step - 1) / step;  // none where kmin is behind the range
+  const Stager<T, DP, BN, WAVES, ALIGNED> stage_k(a.ldk, a.D), stage_v(a.ldv, a.D);
   const auto stage = [&](int n) {
-    L::template stage<BN, WAVES, ALIGNED>(k_tile(n & 1), Kb, a.ldk, kmin + n * BN, a.N, a.D);
-    L::template stage<BN, WAVES, ALIGNED>(v_tile(n & 1), Vb, a.ldv, kmin + n * BN, a.N, a.D);
+    stage_k(k_tile(n & 1), Kb, kmin + n * step, a.N);
+    stage_v(v_tile(n & 1), Vb, kmin + n * step, a.N);
   };
-  stage(0);
+  if (turns > 0) stage(0);
 
   Operand<T> q[QB][NT], go[QB][NT];
   Seq seq[QB];
@@ -535,9 +730,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dq(AttnArgs<T> a) {
     }
     delta[b] = join_halves(s, sum2);
     lse2[b] = a.lse[int64_t(h) * a.N + r] * kLog2e;
-    if (hi == 0 && i < a.N) {
-      a.rows[int64_t(h) * a.N + i] = lse2[b];
-      a.rows[int64_t(a.Hq + h) * a.N + i] = delta[b];
+    if (sp == 0 && hi == 0 && i < a.N) {
+      a.rows[int64_t(2 * h) * a.N + i] = lse2[b];
+      a.rows[int64_t(2 * h + 1) * a.N + i] = delta[b];
     }
   }
   const int first = __builtin_amdgcn_readfirstlane(seq[0].start);
@@ -554,7 +749,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dq(AttnArgs<T> a) {
     wait_vmcnt<0>();
     __syncthreads();
     if (n + 1 < turns) stage(n + 1);
-    const int k0 = kmin + n * BN;
+    const int k0 = kmin + n * step;
     if (k0 + BN <= first || k0 >= w0 + 32 * QB) continue;
     const bool whole = k0 + BN - 1 <= w0 && k0 >= lastStart;
     const char *kt = k_tile(n & 1), *vt = v_tile(n & 1);
@@ -575,18 +770,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dq(AttnArgs<T> a) {
       Operand<T> ds[QB][2];
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
-        const int i = w0 + 32 * b + col;
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const float p = __builtin_amdgcn_exp2f(fmaf(s[b][v], c, -lse2[b]));
           s[b][v] = p * (dp[b][v] - delta[b]);
         }
         if (!whole) {
+          const uint32_t most = w0 + 32 * b + col - seq[b].start, at = k0 + 32 * x + 4 * hi - seq[b].start;
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int j = k0 + 32 * x + mfma32_row(v, hi);
-            s[b][v] = j >= seq[b].start && j <= i ? s[b][v] : 0.f;
-          }
+          for (int v = 0; v < 16; ++v) s[b][v] = at + mfma32_row(v, 0) <= most ? s[b][v] : 0.f;
         }
         ds[b][0] = as_operand<T>(s[b], 0);
         ds[b][1] = as_operand<T>(s[b], 1);
@@ -606,6 +798,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dq(AttnArgs<T> a) {
   for (int b = 0; b < QB; ++b) {
     const int i = w0 + 32 * b + col;
     const bool in = seq[b].inside;
+    if (a.splits > 1) {
+      float* row = a.part + ((int64_t(sp) * a.N + min(i, a.N - 1)) * a.Hq + h) * a.D;
+      if (in) {
+#pragma unroll
+        for (int d = 0; d < NB; ++d) put_block<float, ALIGNED>(row, d, a.D, g[b][d], a.scale);
+      }
+      continue;
+    }
     T* row = a.gQ + int64_t(min(i, a.N - 1)) * a.ldgq + int64_t(h) * a.D;
     if (in) {
 #pragma unroll
@@ -630,8 +830,8 @@ __device__ __forceinline__ void dkv_row(const AttnArgs<T>& a, int kv, int j, int
     const int64_t hd = int64_t(h) * a.D;
     for (int i = j; i < end; ++i) {
       const LaneRow<T> q(a.Q + i * a.ldq + hd, a.D), go(a.gO + i * a.ldgo + hd, a.D);
-      const float p = exp2f(a.scale * kLog2e * q.dot(k) - a.rows[int64_t(h) * a.N + i]);
-      const float ds = p * (go.dot(v) - a.rows[int64_t(a.Hq + h) * a.N + i]) * a.scale;
+      const float p = exp2f(a.scale * kLog2e * q.dot(k) - a.rows[int64_t(2 * h) * a.N + i]);
+      const float ds = p * (go.dot(v) - a.rows[int64_t(2 * h + 1) * a.N + i]) * a.scale;
       ka += ds * q.a;
       kb += ds * q.b;
       va += p * go.a;
@@ -642,8 +842,8 @@ __device__ __forceinline__ void dkv_row(const AttnArgs<T>& a, int kv, int j, int
   put_lanes(a.gV + j * a.ldgv + kd, a.D, va, vb);
 }
 
-template <typename T, int DP, int KB, int WAVES, int BN, bool ALIGNED>
-__global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
+template <typename T, int DP, int KB, int WAVES, int BN, int OCC, bool ALIGNED>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   using L = Tile<T, DP>;
   constexpr int NT = DP / 16, NB = DP / 32, QB = BN / 32, BM = 32 * KB * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -653,7 +853,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
   const auto q_tile = [&](int b) { return smem + b * 2 * TILE; };
   const auto g_tile = [&](int b) { return smem + b * 2 * TILE + TILE; };
 
-  const int t = blockIdx.x / a.Hkv, kv = xcd_swizzle(blockIdx.x % a.Hkv, a.Hkv);
+  const int heads = a.Hkv * a.splits;
+  const int t = blockIdx.x / heads, sp = blockIdx.x % heads / a.Hkv, kv = xcd_swizzle(blockIdx.x % a.Hkv, a.Hkv);
   const int G = a.Hq / a.Hkv;
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
   const int j0 = t * BM, w0 = j0 + wave_id() * 32 * KB;
@@ -661,18 +862,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
 
   const int last = min(j0 + BM, a.N) - 1;
   const int qmax = __builtin_amdgcn_readfirstlane(find_seq(cu, a.S, last, a.N).end);
-  const int per = (qmax - j0 + BN - 1) / BN, turns = per * G;
+  // the tiles of all heads one after the other; the split's are sp, sp + splits, ...
+  const int per = (qmax - j0 + BN - 1) / BN, turns = (per * G - sp + a.splits - 1) / a.splits;
+  const Stager<T, DP, BN, WAVES, ALIGNED> stage_q(a.ldq, a.D), stage_g(a.ldgo, a.D);
   const auto stage = [&](int n) {
-    const int h = kv * G + n / per, i0 = j0 + n % per * BN;
-    L::template stage<BN, WAVES, ALIGNED>(q_tile(n & 1), a.Q + int64_t(h) * a.D, a.ldq, i0, a.N, a.D);
-    L::template stage<BN, WAVES, ALIGNED>(g_tile(n & 1), a.gO + int64_t(h) * a.D, a.ldgo, i0, a.N, a.D);
-    constexpr int UNITS = 2 * BN / 64;
+    const int at = sp + n * a.splits, h = kv * G + at / per, i0 = j0 + at % per * BN;
+    stage_q(q_tile(n & 1), a.Q + int64_t(h) * a.D, i0, a.N);
+    stage_g(g_tile(n & 1), a.gO + int64_t(h) * a.D, i0, a.N);
+    constexpr int UNITS = 2 * BN / 64;  // both rows' statistics, 4 bytes a lane
     if (wave_id() < UNITS) {
       const int x = wave_id() * 64 + lane;
-      copy4_to_lds(a.rows + int64_t((x / BN) * a.Hq + h) * a.N + min(i0 + x % BN, a.N - 1), &stats[n & 1][0][0] + wave_id() * 64);
+      const uint32_t off = (uint32_t(x / BN) * a.N + min(x % BN, a.N - 1 - i0)) * 4;
+      copy_lane4_to_lds(a.rows + int64_t(2 * h) * a.N + i0, off, lds_address(&stats[n & 1][0][0]) + wave_id() * 256);
     }
   };
-  stage(0);
+  if (turns > 0) stage(0);
 
   Operand<T> k[KB][NT], v[KB][NT];
   Seq seq[KB];
@@ -702,7 +906,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
     wait_vmcnt<0>();
     __syncthreads();
     if (n + 1 < turns) stage(n + 1);
-    const int i0 = j0 + n % per * BN;
+    const int i0 = j0 + (sp + n * a.splits) % per * BN;
     if (i0 + BN <= w0 || i0 >= lastEnd) continue;
     const bool whole = i0 >= w0 + 32 * KB - 1 && i0 + BN <= firstEnd;
     const char *qt = q_tile(n & 1), *gt = g_tile(n & 1);
@@ -741,10 +945,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
           dp[b][r] = s[b][r] * (dp[b][r] - delta[r]);
         }
         if (!whole) {
+          // j <= i < end in one comparison
+          const uint32_t most = seq[b].end - j, at = i0 + 32 * x + 4 * hi - j;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int i = i0 + 32 * x + mfma32_row(r, hi);
-            const bool seen = i >= j && i < seq[b].end;
+            const bool seen = at + mfma32_row(r, 0) < most;
             s[b][r] = seen ? s[b][r] : 0.f;
             dp[b][r] = seen ? dp[b][r] : 0.f;
           }
@@ -773,6 +978,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
   for (int b = 0; b < KB; ++b) {
     const int j = w0 + 32 * b + col;
     const bool in = seq[b].inside;
+    if (a.splits > 1) {
+      float* row = a.part + ((int64_t(sp) * a.N + min(j, a.N - 1)) * 2 * a.Hkv + kv) * a.D;
+      if (in) {
+#pragma unroll
+        for (int d = 0; d < NB; ++d) {
+          put_block<float, ALIGNED>(row, d, a.D, gk[b][d], a.scale);
+          put_block<float, ALIGNED>(row + int64_t(a.Hkv) * a.D, d, a.D, gv[b][d], 1.f);
+        }
+      }
+      continue;
+    }
     T* kr = a.gK + int64_t(min(j, a.N - 1)) * a.ldgk + int64_t(kv) * a.D;
     T* vr = a.gV + int64_t(min(j, a.N - 1)) * a.ldgv + int64_t(kv) * a.D;
     if (in) {
@@ -790,6 +1006,36 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_dkv(AttnArgs<T> a) {
   }
 }
 
+// The splits' sums of a row and head, a wave each; looked at again where they are NaN.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs<T> a, int keys) {
+  __shared__ int32_t cu_lds[kCuLds];
+  const int32_t* cu = edges(a.cu, a.S, cu_lds);
+  const int H = keys ? a.Hkv : a.Hq, l = threadIdx.x & 63;
+  const int64_t unit = int64_t(blockIdx.x) * 4 + wave_id();
+  if (unit >= int64_t(a.N) * H) return;
+  const int i = int(unit / H), h = int(unit % H);
+  const Seq seq = find_seq(cu, a.S, i, a.N);
+  if (!seq.inside) return;
+  const int64_t width = int64_t(keys ? 2 : 1) * H * a.D;  // of a partial row
+  const auto sum = [&](T* row, const float* p) {
+    float x = 0.f, y = 0.f;
+    for (int s = 0; s < a.splits; ++s, p += a.N * width) {
+      if (l < a.D) x += p[l];
+      if (l + 64 < a.D) y += p[l + 64];
+    }
+    put_lanes(row, a.D, x, y);
+    return __any(x != x || y != y);
+  };
+  const float* p = a.part + i * width + int64_t(h) * a.D;
+  if (!keys) {
+    if (sum(a.gQ + i * a.ldgq + int64_t(h) * a.D, p)) dq_row(a, h, h / (a.Hq / a.Hkv), i, seq.start);
+  } else {
+    const bool bad = sum(a.gK + i * a.ldgk + int64_t(h) * a.D, p);
+    if (sum(a.gV + i * a.ldgv + int64_t(h) * a.D, p + int64_t(H) * a.D) || bad) dkv_row(a, h, i, seq.end);
+  }
+}
+
 // ------------------------------------------------------------------- launches --
 template <auto K, int LDS, typename T>
 void go(const AttnArgs<T>& a, int64_t blocks, int waves, hipStream_t s) {
@@ -798,21 +1044,51 @@ void go(const AttnArgs<T>& a, int64_t blocks, int waves, hipStream_t s) {
 template <typename T, int DP, int BN>
 constexpr int kLds = 4 * BN * Tile<T, DP>::kRowBytes;  // two buffers of two tiles
 
+constexpr int kWaves = 4, kRows = 32 * kWaves;  // rows of a block of the three kernels
+int64_t row_blocks(int64_t N, int64_t heads) { return (N + kRows - 1) / kRows * heads; }
+
+// Below 256 blocks of 128 rows, one a CU, blocks of 32 rows whose waves share the keys
+// (1024 rows of 8 x 64 bf16: 12.7 against 18.5 us, 2000 of 8 x 128: 35 against 48; with 512
+// blocks, 4096 of 16 x 64, 87 against 68).
 template <typename T, int DP, bool ALIGNED>
 void fwd_t(const AttnArgs<T>& a, hipStream_t s) {
-  constexpr int BN = sizeof(T) == 2 ? 64 : 32;
-  constexpr int QB = 1, W = 4;
-  const int64_t tiles = (int64_t(a.N) + 32 * QB * W - 1) / (32 * QB * W);
-  go<k_attn_fwd<T, DP, QB, W, BN, ALIGNED>, kLds<T, DP, BN>>(a, tiles * a.Hq, W, s);
+  const int64_t blocks = row_blocks(a.N, a.Hq);
+  if (blocks < 256)
+    return go<k_attn_fwd_few<T, DP, kWaves, 1, ALIGNED>, 2 * kRows * Tile<T, DP>::kRowBytes>(
+        a, (int64_t(a.N) + 31) / 32 * a.Hq, kWaves, s);
+  constexpr int BN = sizeof(T) == 2 ? 64 : 32, OCC = sizeof(T) == 2 ? 2 : 1;
+  go<k_attn_fwd<T, DP, 1, kWaves, BN, OCC, ALIGNED>, kLds<T, DP, BN>>(a, blocks, kWaves, s);
 }
+
+// Backward with few blocks: the range of a block is split over several, and their sums
+// are joined by a further launch.  gQ: up to 400 blocks (1999 rows of 6 x 80 fp32, 96 blocks: 194
+// us whole, 74 by 4, 88 by 8).  gK and gV, whose blocks walk over all rows of all heads
+// of a group: up to 1024 (the same with 2 key heads, 32 blocks: 771 us whole, 126 by 8, 104 by 16;
+// 16384 rows of 16 x 64 in 4 key heads, bf16, 512 blocks and sequences of 1 to 4099: 376 us whole, 291
+// by 2, 289 by 4; 8192 rows of 16 x 128, 1024 blocks: 257 whole, 412 by 2).
+int splits(int64_t blocks, int64_t want) { return int(std::max<int64_t>(1, std::min<int64_t>(16, want / blocks))); }
+int dq_splits(int64_t N, int64_t Hq) { return splits(row_blocks(N, Hq), 400); }
+int dkv_splits(int64_t N, int64_t Hkv) { return splits(row_blocks(N, Hkv), 1024); }
+
 template <typename T, int DP, bool ALIGNED>
-void bwd_t(const AttnArgs<T>& a, hipStream_t s) {
-  constexpr int BN = 32;
-  constexpr int QB = 1, W = 4;
-  const int64_t tiles = (int64_t(a.N) + 32 * QB * W - 1) / (32 * QB * W);
-  go<k_attn_dq<T, DP, QB, W, BN, ALIGNED>, kLds<T, DP, BN>>(a, tiles * a.Hq, W, s);
-  go<k_attn_dkv<T, DP, QB, W, BN, ALIGNED>, kLds<T, DP, BN>>(a, tiles * a.Hkv, W, s);
+void bwd_t(AttnArgs<T> a, hipStream_t s) {
+  constexpr bool B = sizeof(T) == 2;
+  constexpr int BN = B ? 64 : 32;
+  a.splits = dq_splits(a.N, a.Hq);
+  go<k_attn_dq<T, DP, 1, kWaves, BN, B ? 2 : 1, ALIGNED>, kLds<T, DP, BN>>(a, row_blocks(a.N, a.Hq) * a.splits, kWaves, s);
+  const auto join = [&](int64_t heads, int keys) {
+    if (a.splits > 1)
+      hipLaunchKernelGGL(k_attn_join<T>, dim3(uint32_t((a.N * heads + 3) / 4)), dim3(256), 0, s, a, keys);
+  };
+  join(a.Hq, 0);
+  a.splits = dkv_splits(a.N, a.Hkv);
+  go<k_attn_dkv<T, DP, 1, kWaves, BN, B && DP <= 64 ? 2 : 1, ALIGNED>, kLds<T, DP, BN>>(
+      a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
+  join(a.Hkv, 1);
 }
+
+// workspace: two floats a row and query head, then the partial sums
+int64_t attn_rows_floats(int64_t N, int64_t Hq) { return (2 * N * Hq + 3) / 4 * 4; }
 
 template <typename T, bool BWD>
 void attn_t(const Attn& c, hipStream_t s) {
@@ -829,6 +1105,8 @@ void attn_t(const Attn& c, hipStream_t s) {
   a.cu = c.cu;
   a.lse = c.lse;
   a.rows = c.rows;
+  a.part = c.rows ? c.rows + attn_rows_floats(c.N, c.Hq) : nullptr;
+  a.splits = 1;
   a.ldq = c.ldq;
   a.ldk = c.ldk;
   a.ldv = c.ldv;
@@ -863,7 +1141,12 @@ void attn_t(const Attn& c, hipStream_t s) {
 }  // namespace
 
 void launch_attn(const Attn& c, int bf16, hipStream_t s) { (bf16 ? attn_t<bf16_t, false> : attn_t<float, false>)(c, s); }
-size_t attn_bwd_ws_bytes(int64_t N, int64_t Hq, int64_t, int64_t) { return size_t(2) * N * Hq * sizeof(float); }
+size_t attn_bwd_ws_bytes(int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (N == 0) return 0;
+  const int64_t q = dq_splits(N, Hq), k = dkv_splits(N, Hkv);
+  const int64_t part = std::max(q > 1 ? q * Hq : 0, k > 1 ? 2 * k * Hkv : 0) * N * D;
+  return size_t(attn_rows_floats(N, Hq) + part) * sizeof(float);
+}
 void launch_attn_bwd(const Attn& c, int bf16, hipStream_t s) { (bf16 ? attn_t<bf16_t, true> : attn_t<float, true>)(c, s); }
 
 }  // namespace mapl

@@ -11,13 +11,13 @@ namespace {
 
 int check_attn_shape(int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
   if (N < 0 || Hkv < 1 || Hq < 1 || Hq > 65536 || Hkv > Hq || Hq % Hkv != 0 || D < 1 || D > 128) return MAPL_ERR_SHAPE;
-  return N > (int64_t(1) << 30) / Hq ? MAPL_ERR_SHAPE : MAPL_OK;
+  return N > (int64_t(1) << 28) || N > (int64_t(1) << 30) / Hq ? MAPL_ERR_SHAPE : MAPL_OK;
 }
 
 // rows of `heads` heads: leading dimensions
 bool short_rows(int64_t heads, int64_t D, std::initializer_list<int64_t> lds) {
   for (int64_t ld : lds)
-    if (ld < heads * D || ld > INT32_MAX) return true;
+    if (ld < heads * D || ld > (int64_t(1) << 22)) return true;  // a tile's rows lie within 2^30 bytes
   return false;
 }
 

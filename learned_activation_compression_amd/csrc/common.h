@@ -31,6 +31,13 @@ __device__ __forceinline__ float bf2f(bf16_t v) { return __uint_as_float(static_
 // Round-to-nearest-even fp32 -> bf16 (hardware v_cvt_pk_bf16_f32 on gfx950).
 __device__ __forceinline__ bf16_t f2bf(float f) { return __builtin_bit_cast(bf16_t, static_cast<__bf16>(f)); }
 
+// two at once, in one instruction
+__device__ __forceinline__ uint32_t cvt2bf(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 __device__ __forceinline__ uint32_t pack2bf(float lo, float hi) {
   return static_cast<uint32_t>(f2bf(lo)) | (static_cast<uint32_t>(f2bf(hi)) << 16);
 }
@@ -93,6 +100,18 @@ __device__ __forceinline__ int xcd_swizzle(int bid, int total) {
 __device__ __forceinline__ void copy16_to_lds(const void* g, const void* l_base) {
   const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(l_base)));
   asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(la) : "memory", "m0");
+}
+
+// Lane l copies 16 (4) bytes from base + lane_off, base uniform over the wave, to LDS
+// byte address lds + 16 l (lds + 4 l); otherwise as copy16_to_lds.
+__device__ __forceinline__ void copy_lane16_to_lds(const void* base, uint32_t lane_off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(lane_off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void copy_lane4_to_lds(const void* base, uint32_t lane_off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(lane_off), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(p)));
 }
 
 // s_waitcnt with only the vector-memory counter limited (gfx9 encoding)

@@ -201,15 +201,6 @@ __global__ __launch_bounds__(256) void k_fp8_unpack(View p, T* X, int64_t rows, 
 }
 
 // ---------------------------------------------------------------------- gemm --
-// Lane l copies 16 (4) bytes from base + 16 l (base + 4 l), base uniform over the
-// wave, to LDS byte address lds + 16 l (lds + 4 l); otherwise as copy16_to_lds.
-__device__ __forceinline__ void copy_lane16_to_lds(const uint8_t* base, uint32_t lane_off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(lane_off), "s"(base), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void copy_lane4_to_lds(const uint8_t* base, uint32_t lane_off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(lane_off), "s"(base), "s"(lds) : "memory", "m0");
-}
-
 __device__ __forceinline__ f32x16 mfma_e4m3(i32x8 a, i32x8 b, f32x16 c, int ea, int eb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, ea, 0, eb);
 }

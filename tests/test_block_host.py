@@ -85,7 +85,7 @@ def test_attention_refusals(lib, call):
     assert call(lib, dt=7) == EDTYPE
     for bad in (dict(N=-1), dict(S=-1), dict(S=2 ** 31 - 1), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(Hq=1), dict(D=0),
                 dict(D=129), dict(N=2 ** 28 + 1), dict(Hq=1 << 17, Hkv=1 << 17), dict(ldq=255), dict(ldk=127), dict(ldv=-128),
-                dict(ldo=2 ** 31)):
+                dict(ldo=2 ** 22 + 1)):
         assert call(lib, **bad) == ESHAPE, bad
     for s in (0.0, -0.1, float("inf"), float("nan")):
         assert call(lib, scale=s) == EARG
@@ -99,7 +99,7 @@ def test_attention_backward_refusals(lib):
     for n in ("gO", "gQ", "gK", "gV", "ws"):
         assert _attn_bwd(lib, N=4, **{n: None}) == ENULL, n
         assert _attn_bwd(lib, N=4, **{n: ODD}) == EARG, n
-    for n, ld in (("ldgo", 255), ("ldgq", 255), ("ldgk", 127), ("ldgv", 2 ** 31)):
+    for n, ld in (("ldgo", 255), ("ldgq", 255), ("ldgk", 127), ("ldgv", 2 ** 22 + 1)):
         assert _attn_bwd(lib, N=4, **{n: ld}) == ESHAPE, n
     assert _attn_bwd(lib, N=4, ws=ctypes.c_void_p(0x1008)) == EARG
     need = lib.stage_attn_bwd_workspace_bytes(4, 4, 2, 64)
@@ -111,7 +111,7 @@ def test_attention_backward_refusals(lib):
 @pytest.mark.parametrize("call", [_attn, _attn_bwd])
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_attention_takes_what_it_documents(lib, call, dt):
-    for kw in (dict(N=1), dict(N=2 ** 28), dict(N=7, D=1), dict(N=7, D=128, ldq=512, ldk=256, ldv=2 ** 31 - 1, ldo=512,
+    for kw in (dict(N=1), dict(N=2 ** 28), dict(N=7, D=1), dict(N=7, D=128, ldq=512, ldk=256, ldv=2 ** 22, ldo=512,
                                                                **(dict(ldgo=512, ldgq=512, ldgk=256, ldgv=256)
                                                                   if call is _attn_bwd else {}))):
         assert call(lib, dt=dt, **kw) == EHIP, kw  # the device set-up's error
