@@ -89,35 +89,36 @@ def stage_norm_pack(X, Y=None, w_post=None, gate=None, w_pre=None, res_scale=1.0
 
 # --------------------------------------------------------------- attention --
 
-def _heads(t, name, index, dtype=None, shape=None):
+def _heads(t, name, index, dtype, shape):
     """Pointer and leading dimension of rows of heads [N, H, D]: heads lie side by side, rows at any stride."""
     try:
-        if t.get_device() == index and (dtype is None or t.dtype is dtype) and t.dim() == 3:
-            N, H, D = t.shape
+        if t.shape == shape and t.dtype is dtype and t.get_device() == index:
             row, head, one = t.stride()
-            if shape is None or t.shape == shape:
-                # torch gives any stride to an axis of one
-                if (one == 1 or D == 1) and (head == D or H == 1) and (row >= H * D or N <= 1):
-                    return t.data_ptr(), row if N > 1 else H * D
-                raise MaplError(-2, "binding", f"{name}: heads must lie side by side and rows apart, strides are {t.stride()}")
-            raise MaplError(-2, "binding", f"{name} must be {list(shape)}, got {list(t.shape)}")
+            N, H, D = shape
+            # torch gives any stride to an axis of one
+            if (one == 1 or D == 1) and (head == D or H == 1) and (row >= H * D or N <= 1):
+                return t.data_ptr(), row if N > 1 else H * D
+            raise MaplError(-2, "binding", f"{name}: heads must lie side by side and rows apart, strides are {t.stride()}")
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MaplError(-1, "binding", f"{name} must be a device tensor")
     if t.get_device() != index:
         raise MaplError(-1, "binding", f"{name} is on {t.device}, not cuda:{index}")
-    if dtype is not None and t.dtype is not dtype:
+    if t.dtype is not dtype:
         raise MaplError(-3, "binding", f"{name} must be {dtype}, got {t.dtype}")
-    raise MaplError(-2, "binding", f"{name} must be [N, heads, D], got {list(t.shape)}")
+    raise MaplError(-2, "binding", f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _attn_shape(Q, K):
-    if not isinstance(Q, torch.Tensor) or not isinstance(K, torch.Tensor):
-        raise MaplError(-1, "binding", "Q and K must be torch.Tensors")
-    if Q.dim() != 3 or K.dim() != 3:
+    """The shapes of Q and its like, and of K and its like."""
+    try:
+        q, k = Q.shape, K.shape
+    except AttributeError:
+        raise MaplError(-1, "binding", "Q and K must be torch.Tensors") from None
+    if len(q) != 3 or len(k) != 3:
         raise MaplError(-2, "binding", "Q and K must be [N, heads, D]")
-    return (*Q.shape, K.shape[1])
+    return q, (q[0], k[1], q[2])
 
 
 def stage_attn(Q, K, V, cu, scale=None, O=None, lse=None, stream=None):
@@ -128,19 +129,22 @@ def stage_attn(Q, K, V, cu, scale=None, O=None, lse=None, stream=None):
     if _elsewhere(cu, "cu", stream):
         with _there(cu, stream):
             return stage_attn(Q, K, V, cu, scale, O, lse)
-    N, Hq, D, Hkv = _attn_shape(Q, K)
+    qs, ks = _attn_shape(Q, K)
+    N, Hq, D = qs
     dev, dt = cu.get_device(), Q.dtype
+    q, ldq = _heads(Q, "Q", dev, dt, qs)
+    k, ldk = _heads(K, "K", dev, dt, ks)
+    v, ldv = _heads(V, "V", dev, dt, ks)
     if O is None:
-        O = torch.empty((N, Hq, D), dtype=dt, device=cu.device)
+        O = Q.new_empty(qs)
+        o, ldo = O.data_ptr(), Hq * D
+    else:
+        o, ldo = _heads(O, "O", dev, dt, qs)
     if lse is None:
-        lse = torch.empty((Hq, N), dtype=torch.float32, device=cu.device)
-    q, ldq = _heads(Q, "Q", dev)
-    k, ldk = _heads(K, "K", dev, dt, (N, Hkv, D))
-    v, ldv = _heads(V, "V", dev, dt, (N, Hkv, D))
-    o, ldo = _heads(O, "O", dev, dt, (N, Hq, D))
+        lse = Q.new_empty((Hq, N), dtype=torch.float32)
     _check(_block_lib().stage_attn(
         q, k, v, _ptr(cu, "cu", dev, torch.int32), o, _ptr(lse, "lse", dev, torch.float32, (Hq, N)),
-        D ** -0.5 if scale is None else float(scale), cu.numel() - 1, N, Hq, Hkv, D, ldq, ldk, ldv, ldo, _dt(Q),
+        D ** -0.5 if scale is None else scale, cu.numel() - 1, N, Hq, ks[1], D, ldq, ldk, ldv, ldo, _dt(Q),
         _raw_stream(dev)), "stage_attn")
     return O, lse
 
@@ -157,25 +161,25 @@ def stage_attn_bwd(gO, Q, K, V, O, lse, cu, scale=None, gQ=None, gK=None, gV=Non
     if _elsewhere(cu, "cu", stream):
         with _there(cu, stream):
             return stage_attn_bwd(gO, Q, K, V, O, lse, cu, scale, gQ, gK, gV, ws)
-    N, Hq, D, Hkv = _attn_shape(Q, K)
-    dev, dt = cu.get_device(), Q.dtype
-    new = lambda H: torch.empty((N, H, D), dtype=dt, device=cu.device)  # noqa: E731
-    gQ = new(Hq) if gQ is None else gQ
-    gK = new(Hkv) if gK is None else gK
-    gV = new(Hkv) if gV is None else gV
-    go, ldgo = _heads(gO, "gO", dev, dt, (N, Hq, D))
-    q, ldq = _heads(Q, "Q", dev)
-    k, ldk = _heads(K, "K", dev, dt, (N, Hkv, D))
-    v, ldv = _heads(V, "V", dev, dt, (N, Hkv, D))
-    o, ldo = _heads(O, "O", dev, dt, (N, Hq, D))
-    gq, ldgq = _heads(gQ, "gQ", dev, dt, (N, Hq, D))
-    gk, ldgk = _heads(gK, "gK", dev, dt, (N, Hkv, D))
-    gv, ldgv = _heads(gV, "gV", dev, dt, (N, Hkv, D))
+    qs, ks = _attn_shape(Q, K)
+    N, Hq, D = qs
+    Hkv, dev, dt = ks[1], cu.get_device(), Q.dtype
+    go, ldgo = _heads(gO, "gO", dev, dt, qs)
+    q, ldq = _heads(Q, "Q", dev, dt, qs)
+    k, ldk = _heads(K, "K", dev, dt, ks)
+    v, ldv = _heads(V, "V", dev, dt, ks)
+    o, ldo = _heads(O, "O", dev, dt, qs)
+    gQ = Q.new_empty(qs) if gQ is None else gQ
+    gK = Q.new_empty(ks) if gK is None else gK
+    gV = Q.new_empty(ks) if gV is None else gV
+    gq, ldgq = _heads(gQ, "gQ", dev, dt, qs)
+    gk, ldgk = _heads(gK, "gK", dev, dt, ks)
+    gv, ldgv = _heads(gV, "gV", dev, dt, ks)
     ws, ws_ptr, ws_size = _bytes(ws, stage_attn_bwd_workspace_bytes(N, Hq, Hkv, D), "ws", cu)
     _check(_block_lib().stage_attn_bwd(
         go, q, k, v, o, _ptr(lse, "lse", dev, torch.float32, (Hq, N)), _ptr(cu, "cu", dev, torch.int32), gq, gk, gv,
-        D ** -0.5 if scale is None else float(scale), cu.numel() - 1, N, Hq, Hkv, D, ldgo, ldq, ldk, ldv, ldo, ldgq,
-        ldgk, ldgv, _dt(Q), ws_ptr, ws_size, _raw_stream(dev)), "stage_attn_bwd")
+        D ** -0.5 if scale is None else scale, cu.numel() - 1, N, Hq, Hkv, D, ldgo, ldq, ldk, ldv, ldo, ldgq, ldgk,
+        ldgv, _dt(Q), ws_ptr, ws_size, _raw_stream(dev)), "stage_attn_bwd")
     return gQ, gK, gV
 
 

@@ -174,29 +174,40 @@ __global__ __launch_bounds__(256) void k_fp8_pack_rows(const T* X, View p, int64
 }
 
 // -------------------------------------------------------------------- unpack --
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-  const uint32_t m = c & 0x7fu;
-  if (m == 0x7fu) return __uint_as_float(0x7fc00000u);
-  const float v = m < 8 ? static_cast<float>(m) * 0.001953125f                       // subnormal: m * 2^-9
-                        : __uint_as_float(((m >> 3) + 120u) << 23 | (m & 7u) << 20);  // 2^(e - 7) (1 + f / 8)
-  return (c & 0x80u) ? -v : v;
-}
-
-// For looking at packs, not for a step's path: one element a store (16384 x 1024 to
-// bf16 in 46 us, to fp32 in 140 us; 10 and 16 us of traffic).
+// As k_fp8_pack_rows: 32 rows x 512 columns a block, 16 columns a thread and step.
+// 16384 x 1024 to bf16 UNPACK_FIGURE.
 template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_unpack(View p, T* X, int64_t rows, int64_t cols) {
-  const uint32_t nkb = static_cast<uint32_t>(p.KB);
-  const int64_t kb = blockIdx.x % nkb, rb = blockIdx.x / nkb;
+  const uint32_t nq = static_cast<uint32_t>((p.KB + 3) / 4);
+  const int64_t kb0 = int64_t(blockIdx.x % nq) * 4, rt = blockIdx.x / nq;
   const int r = threadIdx.x >> 3, j = threadIdx.x & 7;
-  const int64_t c = kb * 128 + 16 * j;
-  for (int64_t rt = rb * 4; rt < rb * 4 + 4; ++rt) {
-    const int64_t row = rt * 32 + r;
-    if (row >= rows) return;
-    const uint8_t* q = p.code + (rt * p.KB + kb) * 4096 + unit_off(r, j);
-    const float s = __uint_as_float(static_cast<uint32_t>(p.exp[kb * p.exp_stride + row]) << 23);
-    for (int i = 0; i < 16; ++i)
-      if (c + i < cols) X[row * cols + c + i] = from_f32<T>(e4m3_value(q[i]) * s);
+  const int64_t row = rt * 32 + r;
+  if (row >= rows) return;
+  u32x4 code[4];
+  uint8_t e[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t kb = min(kb0 + k, p.KB - 1);
+    code[k] = *reinterpret_cast<const u32x4*>(p.code + (rt * p.KB + kb) * 4096 + unit_off(r, j));
+    e[k] = p.exp[kb * p.exp_stride + row];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t c = (kb0 + k) * 128 + 16 * j;
+    if (c >= cols) break;
+    const float s = __uint_as_float(static_cast<uint32_t>(e[k]) << 23);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(code[k][i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(code[k][i], true);
+      v[4 * i] = lo[0] * s;
+      v[4 * i + 1] = lo[1] * s;
+      v[4 * i + 2] = hi[0] * s;
+      v[4 * i + 3] = hi[1] * s;
+    }
+    T* out = X + row * cols + c;
+    store8(out, v, static_cast<int>(min(cols - c, int64_t(8))));
+    if (cols - c > 8) store8(out + 8, v + 8, static_cast<int>(min(cols - c - 8, int64_t(8))));
   }
 }
 
@@ -683,7 +694,7 @@ void launch_fp8_pack(const void* X, uint8_t* pk, uint8_t* pkT, int square, int64
 
 void launch_fp8_unpack(const uint8_t* pk, void* X, int64_t rows, int64_t cols, int bf16, hipStream_t s) {
   const View v(pk, rows, cols);
-  const dim3 grid(uint32_t(v.KB * ((rows + 127) / 128)));
+  const dim3 grid(uint32_t((v.KB + 3) / 4 * v.RT));
   if (bf16)
     hipLaunchKernelGGL(k_fp8_unpack<bf16_t>, grid, dim3(256), 0, s, v, static_cast<bf16_t*>(X), rows, cols);
   else

@@ -186,10 +186,10 @@ def test_loss_refusals_of_one_direction(lib):
     assert _distill(lib, N=4, loss=None) == ENULL and _distill(lib, N=4, loss=ODD) == EARG
     for n in ("gloss", "gZ"):
         assert _distill_bwd(lib, N=4, **{n: None}) == ENULL and _distill_bwd(lib, N=4, **{n: ODD}) == EARG
-    need = lib.stage_distill_workspace_bytes(4, 32000)
+    need = lib.stage_distill_workspace_bytes(4, 131072)
     assert need > 0 and lib.stage_distill_workspace_bytes(4, 100) == 0 and lib.stage_distill_workspace_bytes(5000, 32000) == 0
     assert lib.stage_distill_workspace_bytes(0, 100) == 0 and lib.stage_distill_workspace_bytes(4, -1) == 0
-    big = dict(N=4, V=32000)
+    big = dict(N=4, V=131072)
     assert _distill(lib, **big, ws=None) == ENULL and _distill(lib, **big, ws=ctypes.c_void_p(0x1008)) == EARG
     assert _distill(lib, **big, ws_bytes=need - 1) == EWS
 

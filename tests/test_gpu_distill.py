@@ -59,7 +59,7 @@ def run_both(Z, y, ids, t, g, T=1.0, w_ce=1.0, w_kd=1.0):
 @pytest.mark.parametrize("N, V, K, T", [
     (1, 1, 1, 1.0), (3, 2, 1, 2.0), (5, 7, 3, 1.5), (4, 8, 8, 1.0), (2, 9, 4, 4.0), (7, 255, 16, 2.0), (3, 2047, 64, 0.5),
     (2, 2048, 256, 1.0), (2, 2049, 257, 2.0), (1, 8193, 1024, 1.0), (6, 4096, 1, 8.0), (1300, 33, 5, 2.0), (1100, 2056, 9, 1.5),
-    (2, 32000, 64, 2.0), (3, 32003, 33, 1.0), (1, 131071, 100, 2.0),
+    (2, 32000, 64, 2.0), (3, 32003, 33, 1.0), (1, 131071, 100, 2.0), (2, 70000, 1024, 2.0), (1030, 70, 1024, 3.0),
 ])
 def test_against_the_oracle(N, V, K, T, dt):
     run_both(*make(N, V, K, dt, seed=N + V), T=T, w_ce=0.5, w_kd=0.5 * T * T)
@@ -103,6 +103,12 @@ def test_masked_and_extreme_logits(dt, T):
     Z[2] = -float("inf")
     Z[2, 2499] = 3.0
     Z[3] *= 60.0
+    # a row that is the lowest value throughout: its log-sum is that value in fp32
+    low = torch.full((1, 300), torch.finfo(DT[dt]).min, dtype=DT[dt], device=DEV)
+    l, st = lac.stage_distill(low, torch.zeros(1, dtype=torch.int32, device=DEV))
+    assert torch.isfinite(l).all() and st[0, 0].item() == low[0, 0].item()
+    gl = lac.stage_distill_bwd(torch.ones(1, device=DEV), low, st, torch.zeros(1, dtype=torch.int32, device=DEV))
+    assert torch.isfinite(gl).all()
     ids[0], y[0] = torch.tensor([1, 2, 2450, 99]), 3
     ids[1], y[1] = torch.tensor([0, 1, 2, 3]), 4
     ids[2], y[2] = 2499, 2499
@@ -167,20 +173,21 @@ def test_rows_at_any_address(dt):
 
 
 def test_leading_axes_streams_graphs_and_errors():
-    Z, y, ids, t, g = make(6, 3000, 8, "bf16", seed=6)
+    V = 70000  # two slices a row
+    Z, y, ids, t, g = make(6, V, 8, "bf16", seed=6)
     kw = dict(labels=y, t_ids=ids, t_logits=t, temperature=2.0)
     loss, stats = lac.stage_distill(Z, **kw)
     gZ = lac.stage_distill_bwd(g, Z, stats, **kw)
     kw3 = dict(labels=y.view(2, 3), t_ids=ids.view(2, 3, 8), t_logits=t.view(2, 3, 8), temperature=2.0)
-    l3, s3 = lac.stage_distill(Z.view(2, 3, 3000), **kw3)
-    g3 = lac.stage_distill_bwd(g.view(2, 3), Z.view(2, 3, 3000), s3, **kw3)
-    assert torch.equal(l3.view(6), loss) and torch.equal(g3.view(6, 3000), gZ)
+    l3, s3 = lac.stage_distill(Z.view(2, 3, V), **kw3)
+    g3 = lac.stage_distill_bwd(g.view(2, 3), Z.view(2, 3, V), s3, **kw3)
+    assert torch.equal(l3.view(6), loss) and torch.equal(g3.view(6, V), gZ)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     l2, s2 = lac.stage_distill(Z, stream=s, **kw)
     s.synchronize()
     assert torch.equal(l2, loss) and torch.equal(s2, stats)
-    ws = torch.empty(lac.stage_distill_workspace_bytes(6, 3000), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(lac.stage_distill_workspace_bytes(6, V), dtype=torch.uint8, device=DEV)
     out = [torch.empty_like(x) for x in (loss, stats, gZ)]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
