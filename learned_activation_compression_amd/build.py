@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libmapl.so")
 ARCH = "gfx950"
 
 SOURCES = ["abi.hip", "pack.hip", "codec_bf16.hip", "codec_gemm.hip", "codec_f32.hip", "rvq.hip", "spel.hip", "anchor_grad.hip",
-           "stage.hip", "fp8.hip", "stage_abi.hip", "attn.hip", "distill.hip", "block_abi.hip"]
+           "stage.hip", "fp8.hip", "stage_abi.hip", "attn.hip", "attn_bf16.hip", "distill.hip", "block_abi.hip"]
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 VALU ops.
 COMMON_FLAGS = [
@@ -32,6 +32,11 @@ COMMON_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
+
+# attn_bf16.hip: matrix products leave their result in vector registers, where the softmax reads it,
+# in functions of more than 256 registers too (otherwise copied from accumulation registers and
+# back: gK and gV of 8192 rows of 16 x 128 bf16 in 257 instead of 219 us).
+SOURCE_FLAGS = {"attn_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:
@@ -62,7 +67,7 @@ def build(verbose: bool = False) -> str:
         for src in SOURCES:
             obj = os.path.join(BUILD, src.replace(".hip", ".o"))
             objs.append(obj)
-            cmd = [cc, *COMMON_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = [cc, *COMMON_FLAGS, *SOURCE_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
             jobs.append(ex.submit(_run, cmd, verbose))
         for j in jobs:
             j.result()
