@@ -33,11 +33,6 @@ COMMON_FLAGS = [
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
 
-# attn_bf16.hip: matrix products leave their result in vector registers, where the softmax reads it,
-# in functions of more than 256 registers too (otherwise copied from accumulation registers and
-# back: gK and gV of 8192 rows of 16 x 128 bf16 in 257 instead of 219 us).
-SOURCE_FLAGS = {"attn_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
-
 
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
@@ -67,7 +62,7 @@ def build(verbose: bool = False) -> str:
         for src in SOURCES:
             obj = os.path.join(BUILD, src.replace(".hip", ".o"))
             objs.append(obj)
-            cmd = [cc, *COMMON_FLAGS, *SOURCE_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = [cc, *COMMON_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
             jobs.append(ex.submit(_run, cmd, verbose))
         for j in jobs:
             j.result()

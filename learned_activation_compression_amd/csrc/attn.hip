@@ -1,5 +1,5 @@
 // Causal attention over packed sequences: the fp32 kernels and the launches.  The bf16
-// kernels are compiled apart (attn_bf16.hip), with a flag of their own.
+// kernels are compiled apart (attn_bf16.hip), so that the two build side by side.
 #include "attn_kernels.h"
 
 namespace mapl {

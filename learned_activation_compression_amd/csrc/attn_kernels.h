@@ -287,7 +287,7 @@ struct AttnArgs {
   const T *Q, *K, *V, *O, *gO;
   T *out, *gQ, *gK, *gV;
   const int32_t* cu;
-  float *lse, *rows;  // lse [Hq][N]; rows [Hq][2][N]: lse in units of log 2, and delta
+  float *lse, *rows;  // lse [Hq][N]; rows [Hq][2][N]: -lse / scale and -delta
   float* part;        // sums of a split: gQ [splits][N][Hq D]; gK, gV [splits][N][2][Hkv D]
   int splits;
   int64_t ldq, ldk, ldv, ldo, ldgo, ldgq, ldgk, ldgv;
@@ -754,8 +754,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
     delta[b] = join_halves(s, sum2);
     lse2[b] = a.lse[int64_t(h) * a.N + r] * kLog2e;
     if (sp == 0 && hi == 0 && i < a.N) {
-      a.rows[int64_t(2 * h) * a.N + i] = lse2[b];
-      a.rows[int64_t(2 * h + 1) * a.N + i] = delta[b];
+      a.rows[int64_t(2 * h) * a.N + i] = seq[b].inside ? -a.lse[int64_t(h) * a.N + i] / a.scale : 0.f;
+      a.rows[int64_t(2 * h + 1) * a.N + i] = seq[b].inside ? -delta[b] : 0.f;
     }
   }
   const int first = __builtin_amdgcn_readfirstlane(seq[0].start);
@@ -853,8 +853,8 @@ __device__ __forceinline__ void dkv_row(const AttnArgs<T>& a, int kv, int j, int
     const int64_t hd = int64_t(h) * a.D;
     for (int i = j; i < end; ++i) {
       const LaneRow<T> q(a.Q + i * a.ldq + hd, a.D), go(a.gO + i * a.ldgo + hd, a.D);
-      const float p = exp2f(a.scale * kLog2e * q.dot(k) - a.rows[int64_t(2 * h) * a.N + i]);
-      const float ds = p * (go.dot(v) - a.rows[int64_t(2 * h + 1) * a.N + i]) * a.scale;
+      const float p = exp2f(a.scale * kLog2e * (q.dot(k) + a.rows[int64_t(2 * h) * a.N + i]));
+      const float ds = p * (go.dot(v) + a.rows[int64_t(2 * h + 1) * a.N + i]) * a.scale;
       ka += ds * q.a;
       kb += ds * q.b;
       va += p * go.a;
@@ -871,7 +871,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   constexpr int NT = DP / 16, NB = DP / 32, QB = BN / 32, BM = 32 * KB * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int32_t cu_lds[kCuLds];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][BN];  // log-sum (base 2) and delta
+  __shared__ __attribute__((aligned(16))) float stats[2][2][BN];  // of the tile's rows: -lse / scale and -delta
   constexpr int TILE = BN * L::kRowBytes;
   const auto q_tile = [&](int b) { return smem + b * 2 * TILE; };
   const auto g_tile = [&](int b) { return smem + b * 2 * TILE + TILE; };
@@ -938,8 +938,25 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
       f32x16 s[KB], dp[KB];
+      // the sums begin at the rows' -lse / scale and -delta, so that exp(scale s) is the weight
+      // and the other the difference; fp32 adds the log-sum last, to lose nothing beside it
+      f32x16 y, z;
 #pragma unroll
-      for (int b = 0; b < KB; ++b) s[b] = dp[b] = zero16();
+      for (int r = 0; r < 16; r += 4) {
+        const f32x4 y4 = *reinterpret_cast<const f32x4*>(&stats[n & 1][0][32 * x + 2 * r + 4 * hi]);
+        const f32x4 z4 = *reinterpret_cast<const f32x4*>(&stats[n & 1][1][32 * x + 2 * r + 4 * hi]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[r + e] = y4[e];
+          z[r + e] = z4[e];
+        }
+      }
+      constexpr bool LATE = sizeof(T) == 4;
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        s[b] = LATE ? zero16() : y;
+        dp[b] = z;
+      }
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         const Operand<T> q = L::by_rows(qt, 32 * x, u), go = L::by_rows(gt, 32 * x, u);
@@ -949,25 +966,14 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
           dp[b] = mma(go, v[b][u], dp[b]);
         }
       }
-      float lse2[16], delta[16];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(&stats[n & 1][0][32 * x + 8 * r + 4 * hi]);
-        const f32x4 z = *reinterpret_cast<const f32x4*>(&stats[n & 1][1][32 * x + 8 * r + 4 * hi]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lse2[4 * r + e] = y[e];
-          delta[4 * r + e] = z[e];
-        }
-      }
       Operand<T> p[KB][2], ds[KB][2];
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
         const int j = w0 + 32 * b + col;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, -lse2[r]));
-          dp[b][r] = s[b][r] * (dp[b][r] - delta[r]);
+          s[b][r] = __builtin_amdgcn_exp2f((LATE ? s[b][r] + y[r] : s[b][r]) * c);
+          dp[b][r] *= s[b][r];
         }
         if (!whole) {
           // j <= i < end in one comparison
@@ -1113,20 +1119,22 @@ int splits(int64_t blocks, int64_t want) { return int(std::max<int64_t>(1, std::
 int dq_splits(int64_t N, int64_t Hq) { return splits(row_blocks(N, Hq), 400); }
 int dkv_splits(int64_t N, int64_t Hkv) { return splits(row_blocks(N, Hkv), 1024); }
 
+// Two waves a SIMD in bf16: 256 registers a thread, which hold the widest gK and gV beside
+// tiles of 32 rows only (8192 rows of 16 x 128: 225 us; by 64, one wave a SIMD, 255).  Elsewhere
+// tiles of 64 (16384 rows of 16 x 64: 251 us against 296 by 32; 8192 of 16 x 96: 154, 168).
 template <typename T, int DP, bool ALIGNED>
 void bwd_t(AttnArgs<T> a, hipStream_t s) {
   constexpr bool B = sizeof(T) == 2;
-  constexpr int BN = B ? 64 : 32;
+  constexpr int OCC = B ? 2 : 1, BQ = B ? 64 : 32, BK = B && DP <= 96 ? 64 : 32;
   a.splits = dq_splits(a.N, a.Hq);
-  go<k_attn_dq<T, DP, 1, kWaves, BN, B ? 2 : 1, ALIGNED>, kLds<T, DP, BN>>(a, row_blocks(a.N, a.Hq) * a.splits, kWaves, s);
+  go<k_attn_dq<T, DP, 1, kWaves, BQ, OCC, ALIGNED>, kLds<T, DP, BQ>>(a, row_blocks(a.N, a.Hq) * a.splits, kWaves, s);
   const auto join = [&](int keys) {
     if (a.splits > 1)
       hipLaunchKernelGGL((k_attn_join<T, ALIGNED>), dim3(uint32_t((a.N + kJoin - 1) / kJoin)), dim3(256), 0, s, a, keys);
   };
   join(0);
   a.splits = dkv_splits(a.N, a.Hkv);
-  go<k_attn_dkv<T, DP, 1, kWaves, BN, B && DP <= 64 ? 2 : 1, ALIGNED>, kLds<T, DP, BN>>(
-      a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
+  go<k_attn_dkv<T, DP, 1, kWaves, BK, OCC, ALIGNED>, kLds<T, DP, BK>>(a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
   join(1);
 }
 
