@@ -169,6 +169,7 @@ struct NormArgs {
   int64_t N, rows_per_gate;
   int d;
   View pk;  // of H
+  double inv_d64;
 };
 
 // Largest of 16 neighbouring lanes, the same in each of them
@@ -186,11 +187,7 @@ __device__ __forceinline__ float lane_max16(float v) {
 // in 25.8 us (5.2 TB/s) without and 28 us (4.8 TB/s) with dropout, whose generator
 // does not quite hide; 8192 x 2048 in 28.4 us.  All loads of a row, weights included,
 // are issued before the first sum; the weights come from the caches.
-//
-// PACK: H also leaves as an 8-bit operand.  A thread's 8 columns are a sixteenth of a
-// block of 128, so that a block's largest magnitude is found among 16 neighbouring
-// lanes, and its codes are half of a row's 16-byte piece.
-template <typename T, int TPR, int V, RowMode MODE, bool PACK>
+template <typename T, int TPR, int V, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
   __shared__ float lds[2 * 3 * 16];
@@ -219,7 +216,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) fg[j].issue(g, col(j), a.d);
     }
-    if (PACK || a.H) {
+    if (a.H) {
 #pragma unroll
       for (int j = 0; j < V; ++j) fw[j].issue(a.w_pre, col(j), a.d);
     }
@@ -273,7 +270,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) put_row<MODE>(a.X_out + at, col(j), a.d, in, x[j]);
     }
-    if (PACK || a.H) {
+    if (a.H) {
       float s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -286,22 +283,148 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
         const Raw8<T> w = fw[j].value(col(j), a.d, true);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[j][i] *= r * w.get(i);
-        if (!PACK || a.H) put_row<MODE>(a.H + at, col(j), a.d, in, x[j]);
-        if constexpr (PACK) {
-          if (col(j) + 8 > a.d) {  // a row that is NaN leaves its padding zero
+        put_row<MODE>(a.H + at, col(j), a.d, in, x[j]);
+      }
+    }
+  }
+}
+
+// The same with H as an 8-bit operand.  A thread's 8 columns are a sixteenth of a block of
+// 128: its largest magnitude is found among 16 neighbouring lanes, and its codes are half of
+// a row's 16-byte piece.  e4m3 has few values, and an element near the middle of two goes to
+// one or the other by the last bits of the sums; so the row's roots and the products with
+// them are fp64 (16384 x 1024 bf16 in 28.5 us, 4.1 TB/s; 24.3 in fp32 throughout).
+__device__ __forceinline__ double squares8(const float* v) {  // by pairs: three roundings deep
+  float q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[j][i] = col(j) + i < a.d ? x[j][i] : 0.f;
-          }
-          bool bad;
-          const float top = lane_max16(abs_max<8>(x[j], bad));
-          const int e = block_exp(top);
-          const int64_t kb = col(j) >> 7, rt = n >> 5;
-          if (in && kb < a.pk.KB) {
-            uint8_t* unit = a.pk.code + (rt * a.pk.KB + kb) * 4096 + unit_off(int(n & 31), (col(j) >> 4) & 7);
-            *reinterpret_cast<u32x2*>(unit + (col(j) & 8)) = codes8(x[j], pow2_neg(e), bad);
-            if ((l & 15) == 0) a.pk.exp[kb * a.pk.exp_stride + n] = static_cast<uint8_t>(e);
-          }
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * v[i];
+  return ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+}
+__device__ __forceinline__ double lane_sum16(double v) {
+  const auto dpp = [](double x, auto ctrl) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(
+        double, u32x2{static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(int(w[0]), decltype(ctrl)::value, 0xf, 0xf, false)),
+                      static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(int(w[1]), decltype(ctrl)::value, 0xf, 0xf, false))});
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});
+  v += dpp(v, std::integral_constant<int, 0x4E>{});
+  v += dpp(v, std::integral_constant<int, 0x141>{});
+  return v + dpp(v, std::integral_constant<int, 0x140>{});
+}
+// over a slot, the same in every lane; `lds` [2][16], its halves in turn
+template <int TPR>
+__device__ __forceinline__ double slot_sum64(double v, double* lds, int& turn) {
+  v = lane_sum16(v);
+  if constexpr (TPR >= 32) {
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    const auto lo = __builtin_amdgcn_permlane16_swap(w[0], w[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(w[1], w[1], false, false);
+    v = __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+  }
+  if constexpr (TPR >= 64) {
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[1], false, false);
+    v = __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+  }
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    double* at = lds + (turn & 1) * 16;
+    ++turn;
+    if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += at[threadIdx.x / TPR * W + w];
+  }
+  return v;
+}
+
+template <typename T, int TPR, int V, RowMode MODE>
+__global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_pack(NormArgs<T> a) {
+  constexpr int S = kBlock<TPR> / TPR;
+  __shared__ double lds[2 * 16];
+  int turn = 0;
+  const int l = threadIdx.x % TPR;
+  const auto col = [&](int j) { return 8 * (j * TPR + l); };
+  for (int64_t n0 = int64_t(blockIdx.x) * S; n0 < a.N; n0 += int64_t(gridDim.x) * S) {
+    const int64_t n = n0 + threadIdx.x / TPR;
+    const bool in = n < a.N;
+    const int64_t at = (in ? n : 0) * a.d;
+    Fetch<T, MODE> fx[V], fy[V], fg[V];
+    Fetch<T, MODE == kOdd ? kAny : MODE> fq[V], fw[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      fx[j].issue(a.X + at, col(j), a.d);
+      if (a.Y) fy[j].issue(a.Y + at, col(j), a.d);
+      if (a.w_post) fq[j].issue(a.w_post, col(j), a.d);
+      if (a.gate) fg[j].issue(a.gate + (in ? n / a.rows_per_gate : 0) * a.d, col(j), a.d);
+      fw[j].issue(a.w_pre, col(j), a.d);
+    }
+    double x[V][8];
+    if (a.Y) {
+      float u[V][8];
+      double s = 0.0, q = 1.0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const Raw8<T> r = fy[j].value(col(j), a.d, in);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[j][i] = r.get(i);
+        if (a.dr.t) {
+          const uint32_t keep = keep8(a.dr, static_cast<uint32_t>(j * TPR + l), static_cast<uint64_t>(n));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[j][i] = (keep >> i) & 1 ? u[j][i] * a.dr.scale : 0.f;
         }
+        s += squares8(u[j]);
+      }
+      if (a.w_post) q = rsqrt(fma(slot_sum64<TPR>(s, lds, turn), a.inv_d64, double(a.eps)));
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const Raw8<T> rx = fx[j].value(col(j), a.d, in);
+        Raw8<T> rq, rg;
+        rq.ones();
+        rg.ones();
+        if (a.w_post) rq = fq[j].value(col(j), a.d, true);
+        if (a.gate) rg = fg[j].value(col(j), a.d, true);
+        // three bf16 factors have an exact product in fp32
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[j][i] = fma(double(u[j][i] * (rq.get(i) * rg.get(i))), q, double(a.res_scale) * rx.get(i));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const Raw8<T> r = fx[j].value(col(j), a.d, in);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] = double(a.res_scale) * r.get(i);
+      }
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = MODE == kVec || col(j) + i < a.d ? static_cast<float>(x[j][i]) : 0.f;
+      s += squares8(v);
+      if (a.X_out) put_row<MODE>(a.X_out + at, col(j), a.d, in, v);
+    }
+    const double r = rsqrt(fma(slot_sum64<TPR>(s, lds, turn), a.inv_d64, double(a.eps)));
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const Raw8<T> w = fw[j].value(col(j), a.d, true);
+      float h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = col(j) + i < a.d ? static_cast<float>(x[j][i] * r * w.get(i)) : 0.f;
+      if (a.H) put_row<MODE>(a.H + at, col(j), a.d, in, h);
+      bool bad;
+      const float top = lane_max16(abs_max<8>(h, bad));
+      const int e = block_exp(top);
+      const int64_t kb = col(j) >> 7, rt = n >> 5;
+      if (in && kb < a.pk.KB) {
+        uint8_t* unit = a.pk.code + (rt * a.pk.KB + kb) * 4096 + unit_off(int(n & 31), (col(j) >> 4) & 7);
+        *reinterpret_cast<u32x2*>(unit + (col(j) & 8)) = codes8(h, pow2_neg(e), bad);
+        if ((l & 15) == 0) a.pk.exp[kb * a.pk.exp_stride + n] = static_cast<uint8_t>(e);
       }
     }
   }
@@ -636,18 +759,22 @@ void by_shape(SlotShape sh, const A& args, dim3 grid, hipStream_t s) {
   }
   return L<T, 512, 1>::go(args, grid, s);
 }
-template <typename T, int TPR, int V, bool PACK>
-struct FwdForm {
+template <typename T, int TPR, int V>
+struct FwdLaunch {
   static void go(const NormArgs<T>& a, dim3 grid, hipStream_t s) {
     by_row_mode<T, TPR == 16>(a.d, {a.X, a.Y, a.w_post, a.gate, a.w_pre, a.X_out, a.H}, [&](auto m) {
-      hipLaunchKernelGGL((k_stage_norm<T, TPR, V, decltype(m)::value, PACK>), grid, dim3(kBlock<TPR>), 0, s, a);
+      hipLaunchKernelGGL((k_stage_norm<T, TPR, V, decltype(m)::value>), grid, dim3(kBlock<TPR>), 0, s, a);
     });
   }
 };
 template <typename T, int TPR, int V>
-using FwdLaunch = FwdForm<T, TPR, V, false>;
-template <typename T, int TPR, int V>
-using PackLaunch = FwdForm<T, TPR, V, true>;
+struct PackLaunch {
+  static void go(const NormArgs<T>& a, dim3 grid, hipStream_t s) {
+    by_row_mode<T, TPR == 16>(a.d, {a.X, a.Y, a.w_post, a.gate, a.w_pre, a.X_out, a.H}, [&](auto m) {
+      hipLaunchKernelGGL((k_stage_norm_pack<T, TPR, V, decltype(m)::value>), grid, dim3(kBlock<TPR>), 0, s, a);
+    });
+  }
+};
 template <typename T, int TPR, int V>
 struct BwdLaunch {
   template <bool PRE, bool POST, bool MANY>
@@ -703,6 +830,7 @@ static void norm_t(const StageNorm& c, const uint8_t* pk, hipStream_t s) {
   const uint32_t grid = uint32_t(std::min<int64_t>((c.N + S - 1) / S, 256 * 8));
   if constexpr (PACK) {
     a.pk = View(pk, c.N, c.d);
+    a.inv_d64 = 1.0 / double(c.d);
     by_shape<T, PackLaunch, false>(sh, a, dim3(grid), s);
   } else {
     by_shape<T, FwdLaunch, false>(sh, a, dim3(grid), s);

@@ -1,6 +1,6 @@
 """The block edge with an 8-bit output against its two parts: X_out and H are
-stage_norm's (but for the last bit: which product of a sum is fused into it is the
-compiler's choice in each kernel), and the pack is that of H before rounding."""
+stage_norm's but for the rounding of its fp32 sums (here they are fp64), and the pack
+is that of H before rounding."""
 import numpy as np
 import pytest
 import torch
@@ -36,12 +36,12 @@ def test_fp32_is_its_two_parts(N, G, p, y, d):
     kw = dict(res_scale=0.8, p=p, seed=5, offset=9)
     X_out, H = lac.stage_norm(**a, **kw)
     x, h, pk = lac.stage_norm_pack(**a, **kw, store_h=True)
-    # fused or not, each of the sum's two terms rounds at most twice, and the mean of squares
-    # and the product with the weight add 8 half steps to that
+    # stage_norm's sum of squares is a chain of at most 8 (two vectors: 16) + 6 + 16 additions,
+    # so that its root is off by up to 19 half steps; the products and sums add 5 to that
     size = 0.8 * a["X"].abs() + (X_out - 0.8 * a["X"]).abs()
-    assert torch.all((x - X_out).abs() <= 4 * 2.0 ** -24 * size)
+    assert torch.all((x - X_out).abs() <= 24 * 2.0 ** -24 * size)
     scale = (H / X_out).abs().nan_to_num(posinf=0.0)
-    assert torch.all((h - H).abs() <= 2.0 ** -24 * (8 * H.abs() + 4 * scale * size))
+    assert torch.all((h - H).abs() <= 2.0 ** -24 * (24 * H.abs() + 24 * scale * size))
     want, _ = lac.fp8_pack(h)
     assert torch.equal(values(pk, N, d), values(want, N, d))
     n, none, pk2 = lac.stage_norm_pack(**a, **kw, store_x=False)
