@@ -58,7 +58,7 @@ int stage_norm_pack(const void* X, const void* Y, const void* w_post, const void
  * bf16 for the product with V, their sum is not.
  *
  * 1 <= D <= 128, Hkv >= 1 divides Hq, S >= 0, 0 <= N <= 2^28, N Hq <= 2^30, leading
- * dimensions to 2^22 (MAPL_ERR_SHAPE); scale > 0, finite (MAPL_ERR_ARG).
+ * dimensions to 2^22 (MAPL_ERR_SHAPE); 2^-64 <= scale <= 2^64 (MAPL_ERR_ARG).
  * Outputs may not overlap inputs.
  * The edges are data on the device and are not checked; edges that break the rules
  * give wrong rows, and never an access outside the tensors' N rows.

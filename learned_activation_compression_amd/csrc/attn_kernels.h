@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   // the wave's tiles nb .. ne - 1, from its first row's start to its last row; all of its
   // rows see a tile that begins at or behind the last row's start and ends at or before
   // the first row
-  const int nb = (max(__builtin_amdgcn_readfirstlane(seq[0].start), kmin) - kmin) / BN;
+  const int nb = min((max(__builtin_amdgcn_readfirstlane(seq[0].start), kmin) - kmin) / BN, turns);  // rows beyond N: none
   const int ne = min((w0 + 32 * QB - kmin + BN - 1) / BN, turns);
   const int lastStart = __builtin_amdgcn_readlane(seq[QB - 1].start, 31);
 

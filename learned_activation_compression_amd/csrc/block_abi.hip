@@ -59,7 +59,7 @@ int stage_attn(const void* Q, const void* K, const void* V, const int32_t* cu, v
   if (!dtype_ok(dt)) return MAPL_ERR_DTYPE;
   if (int st = check_attn_shape(N, Hq, Hkv, D)) return st;
   if (S < 0 || S >= INT32_MAX || short_rows(Hq, D, {ldq, ldo}) || short_rows(Hkv, D, {ldk, ldv})) return MAPL_ERR_SHAPE;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return MAPL_ERR_ARG;
+  if (!(scale >= 0x1p-64f && scale <= 0x1p64f)) return MAPL_ERR_ARG;  // its reciprocal and products stay normal
   if (N == 0 || S == 0) return MAPL_OK;
   if (!Q || !K || !V || !cu || !O || !lse) return MAPL_ERR_NULL;
   if (elem_misaligned(dt, {Q, K, V, O}) || elem_misaligned(MAPL_F32, {cu, lse})) return MAPL_ERR_ARG;
@@ -86,7 +86,7 @@ int stage_attn_bwd(const void* gO, const void* Q, const void* K, const void* V, 
   if (int st = check_attn_shape(N, Hq, Hkv, D)) return st;
   if (S < 0 || S >= INT32_MAX || short_rows(Hq, D, {ldgo, ldq, ldo, ldgq}) || short_rows(Hkv, D, {ldk, ldv, ldgk, ldgv}))
     return MAPL_ERR_SHAPE;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return MAPL_ERR_ARG;
+  if (!(scale >= 0x1p-64f && scale <= 0x1p64f)) return MAPL_ERR_ARG;  // its reciprocal and products stay normal
   if (N == 0 || S == 0) return MAPL_OK;
   if (!gO || !Q || !K || !V || !O || !lse || !cu || !gQ || !gK || !gV || !ws) return MAPL_ERR_NULL;
   if (elem_misaligned(dt, {gO, Q, K, V, O, gQ, gK, gV}) || elem_misaligned(MAPL_F32, {cu, lse}) || misaligned(ws, 16))

@@ -87,7 +87,7 @@ def test_attention_refusals(lib, call):
                 dict(D=129), dict(N=2 ** 28 + 1), dict(Hq=1 << 17, Hkv=1 << 17), dict(ldq=255), dict(ldk=127), dict(ldv=-128),
                 dict(ldo=2 ** 22 + 1)):
         assert call(lib, **bad) == ESHAPE, bad
-    for s in (0.0, -0.1, float("inf"), float("nan")):
+    for s in (0.0, -0.1, 2.0 ** -65, 2.0 ** 65, float("inf"), float("nan")):
         assert call(lib, scale=s) == EARG
     for n in ("Q", "K", "V", "cu", "O", "lse"):
         assert call(lib, N=4, **{n: None}) == ENULL, n

@@ -171,3 +171,49 @@ def test_gradient_against_differences():
         # the loss's fp32 errors over the step, and step^2 times third derivatives
         size = (O.double() * go.double()).abs().sum().item()
         assert abs(num - got) <= 64 * F32 * size / step + 30 * step ** 2 * size / lens[1] ** 0.5, (i, num, got)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [2049, 2080, 2081, 2112, 2145, 2175])
+def test_last_block_of_every_fill(N, dt):
+    # the last block of 128 rows holds 1 to 127 of them: some of its waves have no row
+    run([N - 20, 20], 16, 4, 64, dt, seed=N)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** -20, 40.0])
+def test_scales_at_their_ends(scale, dt):
+    lens, Hq, Hkv, D = [300, 40], 2, 1, 64
+    q, k, v, go, cu = make(lens, Hq, Hkv, D, dt, 7)
+    O, lse = lac.stage_attn(q, k, v, cu, scale)
+    g = lac.stage_attn_bwd(go, q, k, v, O, lse, cu, scale)
+    want, size = reference(q, k, v, go, lens, scale)
+    rel = (2 * (D + 4) * size["lse"].max().item() + max(lens) + 8) * F32
+    check(O, want["o"], size["o"], min(rel, 1.0), dt, "o")
+    rel = (2 * (D + 4) * size["lse"].max().item() + 4 * lse.abs().max().item() + 2 * D + 2 * max(lens) + 16) * F32
+    rel += 2.0 ** -8 if dt == "bf16" else F32
+    for x, name in zip(g, ("gq", "gk", "gv")):
+        check(x, want[name], size[name], min(rel, 2.0), dt, name)
+
+
+def test_two_calls_at_once():
+    # two streams, a workspace each: what one leaves in its own does not reach the other
+    lens, Hq, Hkv, D = [1999], 2, 1, 64
+    a, b = make(lens, Hq, Hkv, D, "bf16", 1), make([700, 1299], Hq, Hkv, D, "bf16", 2)
+
+    def both(x, stream=None):
+        q, k, v, go, cu = x
+        O, lse = lac.stage_attn(q, k, v, cu, stream=stream)
+        return (O, lse, *lac.stage_attn_bwd(go, q, k, v, O, lse, cu, stream=stream))
+
+    want = [both(a), both(b)]
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(4):
+        got[0].append(both(a, s))
+        got[1].append(both(b, t))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(x, y) for x, y in zip(w, r))
