@@ -136,7 +136,11 @@ __device__ __forceinline__ void finish(const DistillArgs<T>& a, int64_t n, Sums 
 
 // A block takes a row, or a slice of one where there are few rows.  The teacher's entries
 // and the logits at them are asked for before the row's pass, whose traffic then hides
-// their latency.
+// their latency.  Both sums in one pass, by a running maximum as the reference; about 10
+// vector operations a logit, two of them exp, which take 130 us of 16384 x 32000 bf16 beside the 186
+// of its read: 220-235 us (4.5-4.8 TB/s).  Without the sums the same loads take 177; vectors
+// asked for a turn ahead do not help (231 for 223), and whole turns without their bounds
+// by 3 us.  4 x 32000 fp32: 9.7 us.
 template <typename T, RowMode MODE, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_distill(DistillArgs<T> a) {
   __shared__ Sums sums[THREADS / 64];
@@ -228,7 +232,9 @@ __global__ __launch_bounds__(256) void k_distill_join(DistillArgs<T> a) {
 // The gradient: w1 (softmax(z) - 1[y]) + wT (softmax(z / T) - q).  The row's pass writes
 // the softmaxes; the places of the label and of the teacher's entries are then
 // written again, each by the thread of its first entry with everything that falls on
-// it, from the logit read before the pass (gZ may be Z).
+// it, from the logit read before the pass (gZ may be Z).  Bound by memory: 8192 x 32000 bf16
+// 256 us (4.1 TB/s read and written, a large copy 4.9), 777 x 32003 fp32 39 us (5.1, some of it
+// from the last-level cache).
 template <typename T, RowMode MODE, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_distill_bwd(DistillArgs<T> a) {
   constexpr int J = Teacher<T, THREADS>::J, STEP = 8 * THREADS;

@@ -348,7 +348,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_pack(NormArgs<T> a) 
   int turn = 0;
   const int l = threadIdx.x % TPR;
   const auto col = [&](int j) { return 8 * (j * TPR + l); };
-  for (int64_t n0 = int64_t(blockIdx.x) * S; n0 < a.N; n0 += int64_t(gridDim.x) * S) {
+  // rows behind the last fill its unit of 32 with zeros, as fp8_pack does
+  for (int64_t n0 = int64_t(blockIdx.x) * S; n0 < a.pk.RT * 32; n0 += int64_t(gridDim.x) * S) {
     const int64_t n = n0 + threadIdx.x / TPR;
     const bool in = n < a.N;
     const int64_t at = (in ? n : 0) * a.d;
@@ -415,13 +416,13 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_pack(NormArgs<T> a) 
       const Raw8<T> w = fw[j].value(col(j), a.d, true);
       float h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = col(j) + i < a.d ? static_cast<float>(x[j][i] * r * w.get(i)) : 0.f;
+      for (int i = 0; i < 8; ++i) h[i] = in && col(j) + i < a.d ? static_cast<float>(x[j][i] * r * w.get(i)) : 0.f;
       if (a.H) put_row<MODE>(a.H + at, col(j), a.d, in, h);
       bool bad;
       const float top = lane_max16(abs_max<8>(h, bad));
       const int e = block_exp(top);
       const int64_t kb = col(j) >> 7, rt = n >> 5;
-      if (in && kb < a.pk.KB) {
+      if (n < a.pk.RT * 32 && kb < a.pk.KB) {
         uint8_t* unit = a.pk.code + (rt * a.pk.KB + kb) * 4096 + unit_off(int(n & 31), (col(j) >> 4) & 7);
         *reinterpret_cast<u32x2*>(unit + (col(j) & 8)) = codes8(h, pow2_neg(e), bad);
         if ((l & 15) == 0) a.pk.exp[kb * a.pk.exp_stride + n] = static_cast<uint8_t>(e);
@@ -827,13 +828,13 @@ static void norm_t(const StageNorm& c, const uint8_t* pk, hipStream_t s) {
   a.d = int(c.d);
   const SlotShape sh = slot_shape(c.d, false);
   const int64_t S = slots_per_block(sh);
-  const uint32_t grid = uint32_t(std::min<int64_t>((c.N + S - 1) / S, 256 * 8));
+  const auto grid = [S](int64_t rows) { return dim3(uint32_t(std::min<int64_t>((rows + S - 1) / S, 256 * 8))); };
   if constexpr (PACK) {
     a.pk = View(pk, c.N, c.d);
     a.inv_d64 = 1.0 / double(c.d);
-    by_shape<T, PackLaunch, false>(sh, a, dim3(grid), s);
+    by_shape<T, PackLaunch, false>(sh, a, grid(a.pk.RT * 32), s);
   } else {
-    by_shape<T, FwdLaunch, false>(sh, a, dim3(grid), s);
+    by_shape<T, FwdLaunch, false>(sh, a, grid(c.N), s);
   }
 }
 

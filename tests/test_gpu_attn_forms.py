@@ -217,3 +217,35 @@ def test_two_calls_at_once():
     for w, runs in zip(want, got):
         for r in runs:
             assert all(torch.equal(x, y) for x, y in zip(w, r))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq, Hkv, D, pad", [(4, 2, 128, 0), (6, 2, 40, 1), (256, 256, 16, 0)])
+def test_unseen_values_beside_many_that_are_seen(Hq, Hkv, D, pad, dt):
+    # a row whose sum an unseen NaN has spoilt is formed again over hundreds of visible rows
+    lens = [300, 190]
+    q, k, v, go, cu, O, lse, _ = run(lens, Hq, Hkv, D, dt, pad=pad)
+    want, size = reference(q, k, v, go, lens, D ** -0.5)
+    worst, n = size["lse"].max().item(), max(lens)
+    rel = (2 * (D + 4) * worst + n + 8) * F32
+    others = lambda i: torch.arange(sum(lens), device=DEV) != i  # noqa: E731
+    last, first = others(299), others(300)
+    v2 = v.clone()
+    v2[299] = float("inf")  # seen by row 299 alone
+    O2, lse2 = lac.stage_attn(q, k, v2, cu)
+    check(O2[last], want["o"][last], size["o"][last], rel, dt, "o")
+    assert not torch.isfinite(O2[299]).any() and torch.all((lse2 - lse).abs() <= rel * (1 + lse.abs()))
+    rel = (2 * (D + 4) * worst + 4 * lse.abs().max().item() + 2 * D + n * (Hq // Hkv) + 16) * F32
+    rel += 2.0 ** -8 if dt == "bf16" else F32
+    gq, gk, gv = lac.stage_attn_bwd(go, q, k, v2, O, lse, cu)
+    check(gq[last], want["gq"][last], size["gq"][last], rel, dt, "gq")
+    check(gk[last], want["gk"][last], size["gk"][last], rel, dt, "gk")
+    check(gv, want["gv"], size["gv"], rel, dt, "gv")
+    assert not torch.isfinite(gk[299]).any() and not torch.isfinite(gq[299]).any()  # the only pair of key 299
+    go2 = go.clone()
+    go2[300] = float("nan")  # a factor of key 300's gradients alone
+    gq, gk, gv = lac.stage_attn_bwd(go2, q, k, v, O, lse, cu)
+    check(gq[first], want["gq"][first], size["gq"][first], rel, dt, "gq")
+    check(gk[first], want["gk"][first], size["gk"][first], rel, dt, "gk")
+    check(gv[first], want["gv"][first], size["gv"][first], rel, dt, "gv")
+    assert torch.isnan(gq[300]).all() and torch.isnan(gk[300]).all() and torch.isnan(gv[300]).all()

@@ -139,3 +139,14 @@ def test_padding_streams_graphs_and_errors():
         with pytest.raises(lac.MaplError):
             lac.stage_norm_pack(**{**a, **kw})
     assert lac.stage_norm_pack(a["X"][:0], w_pre=a["w_pre"])[0].shape == (0, d)
+
+
+@pytest.mark.parametrize("N, d", [(1, 128), (33, 200), (40, 1024), (70, 2048), (31, 4100)])
+def test_the_pack_is_the_same_bytes(N, d):
+    # fp8_pack's, with the zeros behind the last row and column; exponents of whole units of 32 rows
+    a = make(N, d, "f32", 1, seed=N)
+    n = lac.fp8_pack_bytes(N, d)
+    pk = [torch.full((n,), 0x7F, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    _, h, _ = lac.stage_norm_pack(**a, store_h=True, pkH=pk[0])
+    lac.fp8_pack(h, pk=pk[1])
+    assert torch.equal(pk[0], pk[1])
