@@ -1090,34 +1090,42 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   }
 }
 
-// The splits' sums, four columns a thread where they are aligned; kJoin rows a block, which
+// The splits' sums, four columns a thread where they are aligned; ROWS rows a block, which
 // looks at its rows again, head by head, where a sum is NaN.  In the order of the splits, so
-// that results repeat.  Bound by memory: 16384 rows of 2 x 4 x 64 by two 15 us, 67 MB of sums read
-// and 17 MB of bf16 written.
-constexpr int kJoin = 8;
-template <typename T, bool ALIGNED>
+// that results repeat.  Bound by memory: 16384 rows of 2 x 4 x 64 by two 16 us, 67 MB of sums read
+// and 17 MB of bf16 written.  8 rows a block there (18 us by 4, 21 by 2: the edges are read
+// by more blocks), 2 where rows are fewer (1999 rows of 2 x 2 x 80 by 16 8.6 us; 16.4 by 8, one
+// split's load behind the other).
+template <typename T, bool ALIGNED, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs<T> a, int keys) {
   constexpr int C = ALIGNED ? 4 : 1;
   __shared__ int32_t cu_lds[kCuLds];
-  __shared__ Seq seq[kJoin];
+  __shared__ Seq seq[ROWS];
   const int32_t* cu = edges(a.cu, a.S, cu_lds);
-  const int H = keys ? a.Hkv : a.Hq, i0 = blockIdx.x * kJoin;
-  if (threadIdx.x < kJoin) seq[threadIdx.x] = find_seq(cu, a.S, i0 + threadIdx.x, a.N);
+  const int H = keys ? a.Hkv : a.Hq, i0 = blockIdx.x * ROWS;
+  if (threadIdx.x < ROWS) seq[threadIdx.x] = find_seq(cu, a.S, i0 + threadIdx.x, a.N);
   __syncthreads();
   const int half = H * a.D, width = keys ? 2 * half : half;  // of a partial row
   const int64_t plane = int64_t(a.N) * width;
   bool bad[2] = {false, false};  // of gQ or gK, and of gV
-  for (int u = threadIdx.x; u < kJoin * (width / C); u += 256) {
+  for (int u = threadIdx.x; u < ROWS * (width / C); u += 256) {
     const int r = u / (width / C), c = u % (width / C) * C;
     if (!seq[r].inside) continue;
     const float* p = a.part + int64_t(i0 + r) * width + c;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.splits; ++s, p += plane) {
+    const auto part = [&](int s) {
       if constexpr (ALIGNED)
-        x += *reinterpret_cast<const f32x4*>(p);
+        return *reinterpret_cast<const f32x4*>(p + s * plane);
       else
-        x[0] += *p;
+        return f32x4{p[s * plane], 0.f, 0.f, 0.f};
+    };
+    int s = 0;
+    for (; s + 4 <= a.splits; s += 4) {
+      const f32x4 y[4] = {part(s), part(s + 1), part(s + 2), part(s + 3)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x += y[k];
     }
+    for (; s < a.splits; ++s) x += part(s);
     T* row = !keys ? a.gQ + (i0 + r) * a.ldgq : c < half ? a.gK + (i0 + r) * a.ldgk : a.gV + (i0 + r) * a.ldgv;
     const int at = c < half ? c : c - half;
     if constexpr (ALIGNED) {
@@ -1131,7 +1139,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs<T> a, int keys) {
   }
   const bool first = __syncthreads_or(bad[0]), second = __syncthreads_or(bad[1]);
   if (!first && !second) return;
-  for (int u = wave_id(); u < kJoin * H; u += 4) {
+  for (int u = wave_id(); u < ROWS * H; u += 4) {
     const int r = u / H, h = u % H;
     if (!seq[r].inside) continue;
     if (!keys) {
@@ -1169,8 +1177,9 @@ void fwd_t(const AttnArgs<T>& a, hipStream_t s) {
 
 // Backward with few blocks: the range of a block is split over several, and their sums
 // are joined by a further launch.  gQ: up to 400 blocks (1999 rows of 6 x 80 fp32, 96 blocks: 194
-// us whole, 74 by 4, 88 by 8).  gK and gV, whose blocks walk over all rows of all heads
-// of a group: up to 1024 (the same with 2 key heads, 32 blocks: 771 us whole, 126 by 8, 104 by 16;
+// us whole, 64 by 4, 69 by 6, 70 by 8, and the join).  gK and gV, whose blocks walk over all rows of
+// all heads of a group: up to 1024 (the same with 2 key heads, 32 blocks: 771 us whole, 126 by 8,
+// 83 by 16, 82 by 24, 94 by 32;
 // 16384 rows of 16 x 64 in 4 key heads, bf16, 512 blocks and sequences of 1 to 4099: 376 us whole, 291
 // by 2, 289 by 4; 8192 rows of 16 x 128, 1024 blocks: 257 whole, 412 by 2).
 int splits(int64_t blocks, int64_t want) { return int(std::max<int64_t>(1, std::min<int64_t>(16, want / blocks))); }
@@ -1187,8 +1196,11 @@ void bwd_t(AttnArgs<T> a, hipStream_t s) {
   a.splits = dq_splits(a.N, a.Hq);
   go<k_attn_dq<T, DP, 1, kWaves, BQ, OCC, ALIGNED>, kLds<T, DP, BQ>>(a, row_blocks(a.N, a.Hq) * a.splits, kWaves, s);
   const auto join = [&](int keys) {
-    if (a.splits > 1)
-      hipLaunchKernelGGL((k_attn_join<T, ALIGNED>), dim3(uint32_t((a.N + kJoin - 1) / kJoin)), dim3(256), 0, s, a, keys);
+    if (a.splits == 1) return;
+    if (a.N >= 8192)
+      hipLaunchKernelGGL((k_attn_join<T, ALIGNED, 8>), dim3(uint32_t((a.N + 7) / 8)), dim3(256), 0, s, a, keys);
+    else
+      hipLaunchKernelGGL((k_attn_join<T, ALIGNED, 2>), dim3(uint32_t((a.N + 1) / 2)), dim3(256), 0, s, a, keys);
   };
   join(0);
   a.splits = dkv_splits(a.N, a.Hkv);
