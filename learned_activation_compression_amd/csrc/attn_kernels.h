@@ -910,12 +910,18 @@ __device__ __forceinline__ void dkv_row(const AttnArgs<T>& a, int kv, int j, int
 // gV = sum_i p gO and gK = scale sum_i p (gO . v - delta) q: four products a pair of rows, a
 // wave's rows being key rows; the query heads of a group one after the other, into the
 // same sums, so that shared heads need no further pass.
-// Bound by issue and, at 128 columns, by registers: K, V, gK and gV of 32 rows are 192 of the
-// 256 that two waves a SIMD leave.  bf16: 16384 rows of 16 x 64 in 4 key heads, sequences of 1 to
-// 4099, 220-235 us and 15 to join (730-780 TFLOP/s); 8192 of 16 x 128, sequences of 2048, 210-225 us
-// (610-655).  K in LDS and 8 waves a block (313 us for 257), operands read ahead of their
-// products (243 for 252 at 64 columns, registers spilled at 128) and masks without a
-// branch (283 for 255) were measured as well.
+// Bound by issue and, at 128 columns, by registers.  bf16: 16384 rows of 16 x 64 in 4 key heads,
+// sequences of 1 to 4099, 220-235 us and 16 to join (730-780 TFLOP/s); 8192 of 16 x 128, sequences
+// of 2048, 156-174 us (790-880).  K in LDS and 8 waves a block (313 us for 257), operands read
+// ahead of their products (243 for 252 at 64 columns, registers spilled at 128) and masks
+// without a branch (283 for 255) were measured as well.
+// K, V, gK and gV of 32 rows of 128 columns are 192 of the 256 registers that two waves a SIMD
+// leave, and one pair of operands at a time can be on its way from LDS.  There V stays in LDS,
+// another read for each of its products: 8192 rows of 16 x 128 156-174 us, 205-225 with V in
+// registers.  Up to 96 columns both fit.
+template <typename T, int DP>
+constexpr bool v_in_lds = sizeof(T) == 2 && DP > 96;
+
 template <typename T, int DP, int KB, int WAVES, int BN, int OCC, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   using L = Tile<T, DP>;
@@ -926,6 +932,8 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   constexpr int TILE = BN * L::kRowBytes;
   const auto q_tile = [&](int b) { return smem + b * 2 * TILE; };
   const auto g_tile = [&](int b) { return smem + b * 2 * TILE + TILE; };
+  constexpr bool VL = v_in_lds<T, DP>;  // the block's rows of V stay in LDS
+  char* const vl = smem + 4 * TILE;
 
   const int heads = a.Hkv * a.splits;
   const int32_t* cu = edges(a.cu, a.S, cu_lds);
@@ -953,8 +961,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
     }
   };
   if (turns > 0) stage(0);
+  if constexpr (VL)  // through registers, which puts zeros behind column D: gO's tile has none there
+    Stager<T, DP, BM, WAVES, false>(a.ldv, a.D)(vl, a.V + int64_t(kv) * a.D, j0, a.N);
 
-  Operand<T> k[KB][NT], v[KB][NT];
+  Operand<T> k[KB][NT], v[KB][VL ? 1 : NT];
   Seq seq[KB];
 #pragma unroll
   for (int b = 0; b < KB; ++b) {
@@ -965,7 +975,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       k[b][u] = load_row<T, ALIGNED>(kr, 16 * u + 8 * hi, a.D);
-      v[b][u] = load_row<T, ALIGNED>(vr, 16 * u + 8 * hi, a.D);
+      if constexpr (!VL) v[b][u] = load_row<T, ALIGNED>(vr, 16 * u + 8 * hi, a.D);
     }
   }
   const int firstEnd = __builtin_amdgcn_readfirstlane(seq[0].end);
@@ -1014,7 +1024,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
           s[b] = mma(q, k[b][u], s[b]);
-          dp[b] = mma(go, v[b][u], dp[b]);
+          if constexpr (VL)
+            dp[b] = mma(go, L::by_rows(vl, 32 * (KB * wave_id() + b), u), dp[b]);
+          else
+            dp[b] = mma(go, v[b][u], dp[b]);
         }
       }
       Operand<T> p[KB][2], ds[KB][2];
@@ -1186,8 +1199,8 @@ int splits(int64_t blocks, int64_t want) { return int(std::max<int64_t>(1, std::
 int dq_splits(int64_t N, int64_t Hq) { return splits(row_blocks(N, Hq), 400); }
 int dkv_splits(int64_t N, int64_t Hkv) { return splits(row_blocks(N, Hkv), 1024); }
 
-// Two waves a SIMD in bf16: 256 registers a thread, which hold the widest gK and gV beside
-// tiles of 32 rows only (8192 rows of 16 x 128: 225 us; by 64, one wave a SIMD, 255).  Elsewhere
+// Two waves a SIMD in bf16: 256 registers a thread, and at 128 columns 80 KB of LDS a block, which
+// the block's V and tiles of 32 rows take (before V was there 225 us; by 64, one wave a SIMD, 255).  Elsewhere
 // tiles of 64 (16384 rows of 16 x 64: 251 us against 296 by 32; 8192 of 16 x 96: 154, 168).
 template <typename T, int DP, bool ALIGNED>
 void bwd_t(AttnArgs<T> a, hipStream_t s) {
@@ -1204,7 +1217,8 @@ void bwd_t(AttnArgs<T> a, hipStream_t s) {
   };
   join(0);
   a.splits = dkv_splits(a.N, a.Hkv);
-  go<k_attn_dkv<T, DP, 1, kWaves, BK, OCC, ALIGNED>, kLds<T, DP, BK>>(a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
+  constexpr int VL = v_in_lds<T, DP> ? kRows * Tile<T, DP>::kRowBytes : 0;
+  go<k_attn_dkv<T, DP, 1, kWaves, BK, OCC, ALIGNED>, kLds<T, DP, BK> + VL>(a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
   join(1);
 }
 
