@@ -4,8 +4,7 @@ Usage:  python -m learned_activation_compression_amd.build [-v]
 
 Each HIP source is compiled to an object under _build/ in parallel, then
 linked into learned_activation_compression_amd/libmapl.so.  Every call
-recompiles (the build is a few seconds per file and the driver uses it as a
-"does it build" check).
+recompiles: the build is its own check that every source compiles.
 """
 from __future__ import annotations
 
