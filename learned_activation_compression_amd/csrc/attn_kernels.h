@@ -22,7 +22,10 @@
 // products are masked or not stored.  A masked product is replaced before the
 // softmax, but a zero weight times an infinity or NaN in a masked place would still
 // spoil a sum of products: an output block that holds a NaN is computed again, row by
-// row over its visible rows alone.  Sums of weights need no such care.
+// row over its visible rows alone.  So are rows with an infinity in a product's padding:
+// behind its D columns an aligned tile repeats a row's first ones, which meet zeros of the
+// other side.  That makes a NaN of a score, and of everything that it enters, so a
+// log-sum that is NaN is formed again as well.
 #pragma once
 
 #include <type_traits>
@@ -372,13 +375,14 @@ struct LaneSum {
 };
 
 // ------------------------------------------------------------------- forward --
+// One row of O, and of lse where `sum_lost`.
 template <typename T>
-__device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int i, int start) {
+__device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int i, int start, bool sum_lost) {
   const T* q = a.Q + i * a.ldq + int64_t(h) * a.D;
   const int64_t kd = int64_t(kv) * a.D;
   float m = -INFINITY, l = 0.f;
   LaneSum o;
-  for (int j = start; j <= i && !o.lost(); j += 64) {
+  for (int j = start; j <= i && (!o.lost() || (sum_lost && l == l)); j += 64) {
     const int n = min(64, i + 1 - j), at = min(int(threadIdx.x & 63), n - 1);
     const float s = a.scale * dot_row(q, a.K + (j + at) * a.ldk + kd, a.D);
     const float mn = fmaxf(m, wave_max(s)), f = m == mn ? 1.f : exp2f((m - mn) * kLog2e);
@@ -390,6 +394,7 @@ __device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int
     o.add(a.V + j * a.ldv + kd, a.ldv, n, p, a.D);
   }
   o.put(a.out + i * a.ldo + int64_t(h) * a.D, a.D, 1.f / l);
+  if (sum_lost && (threadIdx.x & 63) == 0) a.lse[int64_t(h) * a.N + i] = fmaf(__builtin_amdgcn_logf(l), kLn2, m);
 }
 
 // o = sum exp(s - m) v / l with l = sum exp(s - m), in one pass over the keys: a running
@@ -588,9 +593,12 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
       for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, o[b][d], inv);
       if (hi == 0) a.lse[int64_t(h) * a.N + i] = (m[b] * c + __builtin_amdgcn_logf(sum)) * kLn2;
     }
+    // a NaN of the sum is one of a weight, and in every column
     if (any_nan<NB>(o[b], in)) {
       for (int r = 0; r < 32; ++r)
-        if (__builtin_amdgcn_readlane(int(in), r)) fwd_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r));
+        if (__builtin_amdgcn_readlane(int(in), r))
+          fwd_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r),
+                  __builtin_amdgcn_readlane(int(sum != sum), r));
     }
   }
 }
@@ -718,7 +726,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   if (seq.inside && hi == 0 && w == 0) a.lse[int64_t(h) * a.N + i] = (m * c + __builtin_amdgcn_logf(sum)) * kLn2;
   if (__syncthreads_or(seq.inside && bad)) {
     for (int r = w; r < 32; r += WAVES)
-      if (__builtin_amdgcn_readlane(int(seq.inside), r)) fwd_row(a, h, kv, i0 + r, __builtin_amdgcn_readlane(seq.start, r));
+      if (__builtin_amdgcn_readlane(int(seq.inside), r))
+        fwd_row(a, h, kv, i0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(sum != sum), r));
   }
 }
 
