@@ -53,7 +53,9 @@ int stage_norm_pack(const void* X, const void* Y, const void* w_post, const void
  * the three may be columns of one fused projection.  lse [Hq][N], fp32.  Rows
  * outside the sequences are neither read into a result nor written.  What a row
  * does not see never reaches it, infinities and NaN included; among what it sees
- * they act as in the formula (a row that sees only scores of -inf is NaN).
+ * they act as in the formula (a row that sees only scores of -inf is NaN).  Products
+ * q_i . k_j and scores have to be finite in fp32; rows whose largest score is beyond
+ * 2^27 in size are formed one by one, some 250 times as slowly as others.
  * bf16: the weights exp(s_ij - m), m near the row's largest score, are rounded to
  * bf16 for the product with V, their sum is not.
  *
@@ -76,7 +78,9 @@ int stage_attn(const void* Q, const void* K, const void* V, const int32_t* cu, v
  *
  * with h over the query heads that read the key head.  bf16: p_ij and ds_ij are
  * rounded to bf16 for the products; the sums over rows and heads are fp32 and each
- * gradient is rounded once.  Sums have a fixed order: results are bitwise
+ * gradient is rounded once.  lse is a number of 24 bits, so p_ij is off by up to
+ * 2^-21 |lse_i| of itself: less than a rounding to bf16 up to scores of 2^12, worth
+ * nothing (0, infinite or NaN) beyond 2^20.  Sums have a fixed order: results are bitwise
  * repeatable.  `ws` of stage_attn_bwd_workspace_bytes(), 16-byte aligned.  Other rules
  * as for stage_attn. */
 size_t stage_attn_bwd_workspace_bytes(int64_t N, int64_t Hq, int64_t Hkv, int64_t D);

@@ -25,7 +25,7 @@
 // row over its visible rows alone.  So are rows with an infinity in a product's padding:
 // behind its D columns an aligned tile repeats a row's first ones, which meet zeros of the
 // other side.  That makes a NaN of a score, and of everything that it enters, so a
-// log-sum that is NaN is formed again as well.
+// log-sum that is NaN is formed again as well.  And so are rows of very large scores (far).
 #pragma once
 
 #include <type_traits>
@@ -375,6 +375,12 @@ struct LaneSum {
 };
 
 // ------------------------------------------------------------------- forward --
+// The weights exp2(s c - m c) take m c as rounded: a factor that all of a row's weights share,
+// and its sum with them, so that it cancels.  Up to 2^28 it is 2^8 at most, either way;
+// later it would end in 0 or infinity, and the row is formed again, by differences, which
+// for every score would be one vector operation more of 5.
+__device__ __forceinline__ bool far(float m, float c) { return fabsf(m * c) > 0x1p28f && m != -INFINITY; }
+
 // One row of O, and of lse where `sum_lost`.
 template <typename T>
 __device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int i, int start, bool sum_lost) {
@@ -594,11 +600,12 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
       if (hi == 0) a.lse[int64_t(h) * a.N + i] = (m[b] * c + __builtin_amdgcn_logf(sum)) * kLn2;
     }
     // a NaN of the sum is one of a weight, and in every column
-    if (any_nan<NB>(o[b], in)) {
+    const bool lost = sum != sum || far(m[b], c);
+    if (any_nan<NB>(o[b], in) || __any(in && lost)) {
       for (int r = 0; r < 32; ++r)
         if (__builtin_amdgcn_readlane(int(in), r))
           fwd_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r),
-                  __builtin_amdgcn_readlane(int(sum != sum), r));
+                  __builtin_amdgcn_readlane(int(lost), r));
     }
   }
 }
@@ -724,10 +731,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
     if (seq.inside) put4<T, ALIGNED>(row, c0 + e, a.D, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
   }
   if (seq.inside && hi == 0 && w == 0) a.lse[int64_t(h) * a.N + i] = (m * c + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (__syncthreads_or(seq.inside && bad)) {
+  const bool lost = sum != sum || far(m, c);
+  if (__syncthreads_or(seq.inside && (bad || lost))) {
     for (int r = w; r < 32; r += WAVES)
       if (__builtin_amdgcn_readlane(int(seq.inside), r))
-        fwd_row(a, h, kv, i0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(sum != sum), r));
+        fwd_row(a, h, kv, i0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(lost), r));
   }
 }
 

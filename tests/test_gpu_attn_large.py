@@ -1,0 +1,58 @@
+"""Causal attention with scores near the ends of fp32, in both forward forms (blocks
+of 32 rows whose waves share the keys, blocks of 128 rows)."""
+import numpy as np
+import pytest
+import torch
+
+import learned_activation_compression_amd as lac
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+F32 = 2.0 ** -24  # half a step, relative
+FORMS = [([70, 1, 130], 2, 1), ([1100, 1000], 16, 4)]  # few rows; 272 blocks of 128
+
+
+def edges(lens):
+    return torch.tensor(np.cumsum([0, *lens]), dtype=torch.int32, device=DEV)
+
+
+def softmax_rows(q, k, v, lens, scale):
+    """O and lse in float64, head by head."""
+    N, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    o, lse = torch.zeros(q.shape, dtype=torch.float64, device=DEV), torch.zeros(Hq, N, dtype=torch.float64, device=DEV)
+    at = 0
+    for n in lens:
+        r = slice(at, at + n)
+        seen = torch.ones(n, n, dtype=torch.bool, device=DEV).tril()
+        for h in range(Hq):
+            Q, K, V = (x[r, y].double().contiguous() for x, y in ((q, h), (k, h // G), (v, h // G)))
+            s = (scale * (Q @ K.t().contiguous())).masked_fill(~seen, -torch.inf)
+            lse[h, r] = torch.logsumexp(s, 1)
+            o[r, h] = torch.softmax(s, 1) @ V
+        at += n
+    return o, lse
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lens, Hq, Hkv", FORMS)
+@pytest.mark.parametrize("D, size, scale", [(64, 8, 2.0 ** 12), (64, 8, 2.0 ** 22), (64, 8, 2.0 ** 28), (64, 8, 2.0 ** 34),
+                                            (64, 8, 2.0 ** 64), (80, 8, 2.0 ** 64), (64, 2.0 ** 17, 0.125),
+                                            (128, 2.0 ** 22, 0.125)])
+def test_scores_of_the_largest_size(D, size, scale, lens, Hq, Hkv, dt):
+    # few bits a factor, so that every score is exact: keys of a row's largest score share its
+    # weight, and no other, a unit of 2^12 away at least, has any
+    g = torch.Generator(device=DEV).manual_seed(D)
+    N = sum(lens)
+    q, k = ((torch.randint(-8, 9, (N, h, D), generator=g, device=DEV) * (size / 8)).to(DT[dt]) for h in (Hq, Hkv))
+    v = torch.randn(N, Hkv, D, generator=g, device=DEV).to(DT[dt])
+    k[5], k[lens[0] + 3] = k[0], k[lens[0]]  # and some shared
+    want, wlse = softmax_rows(q, k, v, lens, scale)
+    O, lse = lac.stage_attn(q, k, v, edges(lens), scale)
+    assert torch.isfinite(O).all() and torch.isfinite(lse).all()
+    # one key, or a mean of few: the mean's roundings and the output's
+    half = 2 * 2.0 ** -8 if dt == "bf16" else 16 * F32
+    assert torch.all((O.double() - want).abs() <= half * v.double().abs().max()), (O.double() - want).abs().max()
+    # the scale times log2 e, the largest score by it, and back: four roundings, and the output's
+    assert torch.all((lse.double() - wlse).abs() <= 6 * F32 * wlse.abs() + 2 * F32)
