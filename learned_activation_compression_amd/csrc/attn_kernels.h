@@ -25,7 +25,9 @@
 // row over its visible rows alone.  So are rows with an infinity in a product's padding:
 // behind its D columns an aligned tile repeats a row's first ones, which meet zeros of the
 // other side.  That makes a NaN of a score, and of everything that it enters, so a
-// log-sum that is NaN is formed again as well.  And so are rows of very large scores (far).
+// log-sum that is NaN is formed again as well.  And so are rows of very large scores (far)
+// and those whose sum of weighted values, up to 2^8 times their number of keys as large as
+// its mean, is infinite: by means of the keys so far, which are no larger than the values.
 #pragma once
 
 #include <type_traits>
@@ -331,13 +333,14 @@ __device__ __forceinline__ void put_block(T* row, int db, int D, const f32x16& x
     put4<T, ALIGNED>(row, 32 * db + 8 * g + 4 * h, D, x[4 * g] * f, x[4 * g + 1] * f, x[4 * g + 2] * f, x[4 * g + 3] * f);
 }
 
-template <int NB>
-__device__ __forceinline__ bool any_nan(const f32x16 (&x)[NB], bool in) {
+// of the lanes `in`; FINITE: infinities too
+template <bool FINITE, int NB>
+__device__ __forceinline__ bool any_bad(const f32x16 (&x)[NB], bool in) {
   bool bad = false;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) bad = bad || x[b][v] != x[b][v];
+    for (int v = 0; v < 16; ++v) bad = bad || (FINITE ? !(fabsf(x[b][v]) < INFINITY) : x[b][v] != x[b][v]);
   return __any(in && bad);
 }
 
@@ -393,13 +396,15 @@ __device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int
     const float s = a.scale * dot_row(q, a.K + (j + at) * a.ldk + kd, a.D);
     const float mn = fmaxf(m, wave_max(s)), f = m == mn ? 1.f : exp2f((m - mn) * kLog2e);
     const float p = int(threadIdx.x & 63) >= n || s == -INFINITY ? 0.f : exp2f((s - mn) * kLog2e);
+    const float before = l * f;
     m = mn;
-    l = l * f + wave_sum(p);
-    o.a *= f;
-    o.b *= f;
-    o.add(a.V + j * a.ldv + kd, a.ldv, n, p, a.D);
+    l = before + wave_sum(p);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no weight yet: the sums stay 0
+    o.a *= before * inv;
+    o.b *= before * inv;
+    o.add(a.V + j * a.ldv + kd, a.ldv, n, p * inv, a.D);
   }
-  o.put(a.out + i * a.ldo + int64_t(h) * a.D, a.D, 1.f / l);
+  o.put(a.out + i * a.ldo + int64_t(h) * a.D, a.D, l == 0.f ? NAN : 1.f);
   if (sum_lost && (threadIdx.x & 63) == 0) a.lse[int64_t(h) * a.N + i] = fmaf(__builtin_amdgcn_logf(l), kLn2, m);
 }
 
@@ -601,7 +606,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
     }
     // a NaN of the sum is one of a weight, and in every column
     const bool lost = sum != sum || far(m[b], c);
-    if (any_nan<NB>(o[b], in) || __any(in && lost)) {
+    if (any_bad<true>(o[b], in) || __any(in && lost)) {
       for (int r = 0; r < 32; ++r)
         if (__builtin_amdgcn_readlane(int(in), r))
           fwd_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r),
@@ -726,7 +731,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
       y[k] = 0.f;
 #pragma unroll
       for (int x = 0; x < WAVES; ++x) y[k] += f[x] * part[(x * DP + c0 + e + k) * 32 + col];
-      bad = bad || (c0 + e + k < a.D && y[k] != y[k]);
+      bad = bad || (c0 + e + k < a.D && !(fabsf(y[k]) < INFINITY));
     }
     if (seq.inside) put4<T, ALIGNED>(row, c0 + e, a.D, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
   }
@@ -895,7 +900,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
 #pragma unroll
       for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, g[b][d], a.scale);
     }
-    if (any_nan<NB>(g[b], in)) {
+    if (any_bad<false>(g[b], in)) {
       for (int r = 0; r < 32; ++r)
         if (__builtin_amdgcn_readlane(int(in), r)) dq_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r));
     }
@@ -1110,7 +1115,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
         put_block<T, ALIGNED>(vr, d, a.D, gv[b][d], 1.f);
       }
     }
-    const bool bad_k = any_nan<NB>(gk[b], in), bad_v = any_nan<NB>(gv[b], in);
+    const bool bad_k = any_bad<false>(gk[b], in), bad_v = any_bad<false>(gv[b], in);
     for (int r = 0; (bad_k || bad_v) && r < 32; ++r) {
       if (!__builtin_amdgcn_readlane(int(in), r)) continue;
       const int end = __builtin_amdgcn_readlane(seq[b].end, r);

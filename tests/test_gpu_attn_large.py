@@ -1,5 +1,5 @@
-"""Causal attention with scores near the ends of fp32, in both forward forms (blocks
-of 32 rows whose waves share the keys, blocks of 128 rows)."""
+"""Causal attention with scores and values near the ends of fp32, in both forward
+forms (blocks of 32 rows whose waves share the keys, blocks of 128 rows)."""
 import numpy as np
 import pytest
 import torch
@@ -56,3 +56,23 @@ def test_scores_of_the_largest_size(D, size, scale, lens, Hq, Hkv, dt):
     assert torch.all((O.double() - want).abs() <= half * v.double().abs().max()), (O.double() - want).abs().max()
     # the scale times log2 e, the largest score by it, and back: four roundings, and the output's
     assert torch.all((lse.double() - wlse).abs() <= 6 * F32 * wlse.abs() + 2 * F32)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lens, Hq, Hkv", FORMS)
+@pytest.mark.parametrize("D", [40, 64, 128])
+def test_values_near_the_largest(D, lens, Hq, Hkv, dt):
+    # a mean of values lies among them, whatever their sum
+    g = torch.Generator(device=DEV).manual_seed(D)
+    N = sum(lens)
+    q = torch.full((N, Hq, D), 1.0, device=DEV).to(DT[dt])
+    # scores rise by up to 5 over the sequence: late weights are far above the first
+    k = (torch.linspace(0, 5, N, device=DEV)[:, None, None] / D ** 0.5).expand(N, Hkv, D).contiguous().to(DT[dt])
+    v = ((0.5 + 0.5 * torch.rand(N, Hkv, D, generator=g, device=DEV)) * 2.0 ** 127).to(DT[dt])
+    want, wlse = softmax_rows(q, k, v, lens, D ** -0.5)
+    O, lse = lac.stage_attn(q, k, v, edges(lens))
+    n, worst = max(lens), 5.1
+    # all terms of one sign: the sum of sizes is the output; scores to (D + 4) half steps of theirs
+    rel = (2 * (D + 4) * worst + n + 16) * F32 + (2 * 2.0 ** -8 if dt == "bf16" else F32)
+    assert torch.isfinite(O).all() and torch.all((O.double() - want).abs() <= rel * want)
+    assert torch.all((lse.double() - wlse).abs() <= ((D + 4) * worst + 4 * wlse.abs() + n + 8) * F32)
