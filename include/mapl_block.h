@@ -123,7 +123,9 @@ int stage_distill(const void* Z, const int32_t* labels, const int32_t* t_ids, co
  *               + w_kd / T (exp(z_v / T - lse_T) - sum_{k: id_k = v} q_k))
  *
  * with the absent terms left out; a row of neither label nor entries is 0 whatever
- * its logits.  Each element is rounded once.  gZ may be Z.  Other rules as for
+ * its logits.  lse and lse_T are numbers of 24 bits, so the softmaxes are off by up to
+ * 2^-22 |lse| (2^-22 |lse_T|) of themselves: the loss does not depend on an offset that all of
+ * a row's logits share, but a gradient beside one of 2^16 has six bits left.  Each element is rounded once.  gZ may be Z.  Other rules as for
  * stage_distill. */
 int stage_distill_bwd(const float* gloss, const void* Z, const float* stats, const int32_t* labels,
                       const int32_t* t_ids, const float* t_logits, void* gZ, float temperature, float w_ce, float w_kd,

@@ -69,7 +69,7 @@ __device__ __forceinline__ float sum2(float x, float y) { return x + y; }
 __device__ __forceinline__ float max2(float x, float y) { return fmaxf(x, y); }
 
 // The teacher's entries k = threadIdx.x + THREADS j of a row: their ids (-1: none), their
-// scaled logits and the student's logits there.  An entry with a logit of -inf has none.
+// logits and the student's logits there.  An entry with a logit of -inf has none.
 // Everything that memory has to bring is asked for at once, and early.
 template <typename T, int THREADS>
 struct Teacher {
@@ -85,7 +85,7 @@ struct Teacher {
       if (THREADS * j < a.K) {
         const int64_t at = n * a.K + min(k, a.K - 1);
         const int i = a.t_ids[at];
-        x[j] = a.t_logits[at] * a.inv_T;
+        x[j] = a.t_logits[at];
         if (k < a.K && i >= 0 && i < a.V && x[j] != -INFINITY) id[j] = i;
       }
     }
@@ -93,44 +93,47 @@ struct Teacher {
     for (int j = 0; j < J; ++j)
       if (THREADS * j < a.K) z[j] = to_f32<T>(a.Z[n * a.V + max(id[j], 0)]);
   }
-  // the probabilities e / s of the entries, e = 2^(x - top); s = 0: no entry
+  // the probabilities e / s of the entries, e = exp((x - top) / T); s = 0: no entry
   __device__ __forceinline__ float norm(const DistillArgs<T>& a, float* lds, float& top, float (&e)[J]) {
     top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (THREADS * j < a.K && id[j] >= 0) top = fmaxf(top, x[j]);
     top = block_all<THREADS>(top, lds, max2);
+    const float cT = kLog2e * a.inv_T;
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      e[j] = THREADS * j < a.K && id[j] >= 0 ? ex2((x[j] - top) * kLog2e) : 0.f;
+      e[j] = THREADS * j < a.K && id[j] >= 0 ? ex2((x[j] - top) * cT) : 0.f;
       s += e[j];
     }
     return block_all<THREADS>(s, lds + 16, sum2);
   }
 };
 
+// Log-sums and logits enter the loss as differences from the largest logit, the teacher's
+// from its own: rounded beside a common offset they would lose the loss.
 template <typename T, int THREADS>
 __device__ __forceinline__ void finish(const DistillArgs<T>& a, int64_t n, Sums v, const Teacher<T, THREADS>& t, float zy,
                                        bool label, float* lds) {
-  const float lse1 = fmaf(lg2(v.s1), kLn2, ref(v.m));
-  const float lseT = a.warm ? fmaf(lg2(v.sT), kLn2, ref(v.m) * a.inv_T) : lse1;
+  const float m = ref(v.m), log1 = lg2(v.s1) * kLn2, logT = a.warm ? lg2(v.sT) * kLn2 : log1;
   float loss = 0.f;
   if (a.w_kd != 0.f && a.K > 0) {
     Teacher<T, THREADS> u = t;
     float e[Teacher<T, THREADS>::J], top, kd = 0.f;
-    const float s = u.norm(a, lds, top, e), l = top + lg2(s) * kLn2;
+    const float s = u.norm(a, lds, top, e), l = lg2(s) * kLn2;
 #pragma unroll
     for (int j = 0; j < Teacher<T, THREADS>::J; ++j)
-      if (THREADS * j < a.K && e[j] != 0.f) kd += e[j] * ((u.x[j] - l) - (u.z[j] * a.inv_T - lseT));
+      if (THREADS * j < a.K && e[j] != 0.f) kd += e[j] * (((u.x[j] - top) * a.inv_T - l) - ((u.z[j] - m) * a.inv_T - logT));
     kd = block_all<THREADS>(kd, lds + 32, sum2);
     if (s != 0.f) loss = a.w_kd * (kd / s);
   }
   if (threadIdx.x == 0) {
-    if (label) loss += a.w_ce * (lse1 - zy);
+    if (label) loss += a.w_ce * ((m - zy) + log1);
     a.loss[n] = loss;
+    const float lse1 = fmaf(lg2(v.s1), kLn2, m);
     a.stats[2 * n] = lse1;
-    a.stats[2 * n + 1] = lseT;
+    a.stats[2 * n + 1] = a.warm ? fmaf(lg2(v.sT), kLn2, m * a.inv_T) : lse1;
   }
 }
 
