@@ -25,10 +25,12 @@ extern "C" {
  *
  *   pkH = the pack of H [N][d] as fp8_pack makes it with square = 0,
  *
- * from H before any rounding to dt.  X_out and H are stored where they are not
- * NULL (a backward pass needs X_out, and H for the transposed operand of the
- * weight gradient); w_pre is required.  pkH is 16-byte aligned (MAPL_ERR_ARG) and of
- * fp8_pack_bytes(N, d) (MAPL_ERR_WORKSPACE), sizes as for both.  The backward pass is that of stage_norm.
+ * from H before its rounding to bf16 (fp32: of H as it is stored).  The rows' roots
+ * and the products with them are fp64; bf16 outputs, and codes beside them, are
+ * rounded once from there.  X_out and H are stored where they are not NULL (a backward
+ * pass needs X_out, and H for the transposed operand of the weight gradient); w_pre is
+ * required.  pkH is 16-byte aligned (MAPL_ERR_ARG) and of fp8_pack_bytes(N, d)
+ * (MAPL_ERR_WORKSPACE), sizes as for both.  The backward pass is that of stage_norm.
  * Other rules as for stage_norm.
  * ---------------------------------------------------------------------- */
 int stage_norm_pack(const void* X, const void* Y, const void* w_post, const void* gate, const void* w_pre,
@@ -124,9 +126,9 @@ int stage_distill(const void* Z, const int32_t* labels, const int32_t* t_ids, co
  *
  * with the absent terms left out; a row of neither label nor entries is 0 whatever
  * its logits.  lse and lse_T are numbers of 24 bits, so the softmaxes are off by up to
- * 2^-22 |lse| (2^-22 |lse_T|) of themselves: the loss does not depend on an offset that all of
- * a row's logits share, but a gradient beside one of 2^16 has six bits left.  Each element is rounded once.  gZ may be Z.  Other rules as for
- * stage_distill. */
+ * 2^-22 |lse| (2^-22 |lse_T|) of themselves: an offset that all of a row's logits share
+ * does not count in the loss, but one of 2^16 leaves a gradient six bits.  Each element
+ * is rounded once.  gZ may be Z.  Other rules as for stage_distill. */
 int stage_distill_bwd(const float* gloss, const void* Z, const float* stats, const int32_t* labels,
                       const int32_t* t_ids, const float* t_logits, void* gZ, float temperature, float w_ce, float w_kd,
                       int64_t N, int64_t V, int64_t K, mapl_dtype dt, hipStream_t stream);

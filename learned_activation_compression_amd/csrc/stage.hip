@@ -341,6 +341,19 @@ __device__ __forceinline__ double slot_sum64(double v, double* lds, int& turn) {
   return v;
 }
 
+// A double as the float that a rounding to fewer bits takes: to 24 bits by rounding to odd
+// (the last bit is set if any behind it was), which no middle of two shorter numbers is,
+// so that the rounding behind it falls as the double's would.  An fp32 output, and the
+// pack of it, is the double rounded to nearest.
+template <typename T>
+__device__ __forceinline__ float for_rounding(double x) {
+  if constexpr (sizeof(T) == 4) return static_cast<float>(x);
+  u32x2 w = __builtin_bit_cast(u32x2, x);
+  constexpr uint32_t below = (1u << 29) - 1;  // the 29 bits that a float of this size has not
+  w[0] = (w[0] | ((w[0] & below) + below)) & ~below;
+  return static_cast<float>(__builtin_bit_cast(double, w));
+}
+
 template <typename T, int TPR, int V, RowMode MODE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_pack(NormArgs<T> a) {
   constexpr int S = kBlock<TPR> / TPR;
@@ -406,7 +419,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_pack(NormArgs<T> a) 
     for (int j = 0; j < V; ++j) {
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = MODE == kVec || col(j) + i < a.d ? static_cast<float>(x[j][i]) : 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = MODE == kVec || col(j) + i < a.d ? for_rounding<T>(x[j][i]) : 0.f;
       s += squares8(v);
       if (a.X_out) put_row<MODE>(a.X_out + at, col(j), a.d, in, v);
     }
@@ -416,7 +429,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm_pack(NormArgs<T> a) 
       const Raw8<T> w = fw[j].value(col(j), a.d, true);
       float h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = in && col(j) + i < a.d ? static_cast<float>(x[j][i] * r * w.get(i)) : 0.f;
+      for (int i = 0; i < 8; ++i) h[i] = in && col(j) + i < a.d ? for_rounding<T>(x[j][i] * r * w.get(i)) : 0.f;
       if (a.H) put_row<MODE>(a.H + at, col(j), a.d, in, h);
       bool bad;
       const float top = lane_max16(abs_max<8>(h, bad));
