@@ -82,3 +82,58 @@ def test_teachers_entries_of_the_lowest_value(V, T):
     g = torch.ones(3, device=DEV)
     ga, gb = lac.stage_distill_bwd(g, Z, a[1], y, ids, t, T), lac.stage_distill_bwd(g, Z, b[1], y, two, even, T)
     assert torch.equal(ga, gb)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [70000, 131071])
+@pytest.mark.parametrize("T", [1.0, 2.0])
+def test_slices_that_hold_nothing(T, V, dt):
+    # forward two and three slices a row, backward 17 and 31: some of them -inf throughout
+    g = torch.Generator().manual_seed(V)
+    N, K = 6, 5
+    assert lac.stage_distill_workspace_bytes(N, V) > 0
+    Z = (3 * torch.randn(N, V, generator=g)).clamp(-12, 12).to(DEV, DT[dt])
+    Z[0, :V // 2] = -float("inf")             # the first slices
+    Z[1, :-1], Z[1, -1] = -float("inf"), 2.0  # a single finite logit, the last
+    Z[2, 3:] = torch.finfo(DT[dt]).min        # the lowest value from the third on
+    Z[3, 8:] = -float("inf")                  # all but the first vector
+    Z[4, V - 9:] = -float("inf")
+    ids = torch.randint(0, V, (N, K), generator=g, dtype=torch.int32)
+    y = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    ids[0] = torch.arange(V - K, V)
+    ids[1], y[1] = torch.tensor([V - 1, -1, V - 1, -1, -1]), V - 1
+    ids[2], y[2] = torch.tensor([0, 1, 2, 1, -1]), 2
+    ids[3], y[3] = torch.tensor([0, 7, 3, 4, 5]), 7
+    ids[4], y[4], y[0] = torch.arange(K), V // 2, V - 2
+    t, go = torch.randn(N, K, generator=g), torch.randn(N, generator=g)
+    y, ids, t, go = (x.to(DEV) for x in (y, ids, t, go))
+    a = (np64(y).astype(int), np64(ids).astype(int), np64(t), T, 0.5, 0.5)
+    want, wstats, _ = block.distill(np64(Z), *a)
+    loss, stats = lac.stage_distill(Z, y, ids, t, T, 0.5, 0.5)
+    # finite logits of 12 in size: sums by chains of V / 256 + 64 additions, exponents and
+    # differences of a few roundings each
+    rel = (V / 256 + 64 + 8 * 24 * max(1.0, 1 / T) + 8 * np.log(V)) * F32
+    assert np.all(np.abs(np64(stats) - wstats) <= 2 * rel)
+    assert np.all(np.abs(np64(loss) - want) <= 4 * rel * (1 + np.abs(want)))
+    gw, gsize = block.distill_bwd(np64(go), np64(Z), *a)
+    gZ = lac.stage_distill_bwd(go, Z, stats, y, ids, t, T, 0.5, 0.5)
+    half = 2.0 ** -8 if dt == "bf16" else F32
+    assert np.all(np.abs(np64(gZ) - gw) <= 4 * rel * gsize + half * np.abs(gw) + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_slices_of_rows_do_not_mix(bad):
+    # a value that is not finite in one slice reaches its own row, and no other
+    g = torch.Generator().manual_seed(1)
+    N, V = 4, 70000
+    Z = torch.randn(N, V, generator=g).to(DEV)
+    y = torch.randint(0, V, (N,), generator=g, dtype=torch.int32).to(DEV)
+    go = torch.randn(N, generator=g).to(DEV)
+    a = lac.stage_distill(Z, y)
+    ga = lac.stage_distill_bwd(go, Z, a[1], y)
+    Z[2, 60000] = bad
+    b = lac.stage_distill(Z, y)
+    gb = lac.stage_distill_bwd(go, Z, b[1], y)
+    keep = [0, 1, 3]
+    assert torch.equal(a[0][keep], b[0][keep]) and torch.equal(a[1][keep], b[1][keep]) and torch.equal(ga[keep], gb[keep])
+    assert not torch.isfinite(b[0][2]) and not torch.isfinite(b[1][2]).any()
