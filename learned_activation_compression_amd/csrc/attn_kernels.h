@@ -419,10 +419,10 @@ __device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int
 // bf16: 16384 rows of 16 x 64 in sequences of 2048 101 us (681 TFLOP/s of unmasked pairs),
 // 16384 rows of 16 x 128 in one sequence 1.03-1.09 ms (1.01-1.07 PFLOP/s; the library's product
 // of 16384^3 reaches 1.40).
-template <typename T, int DP, int QB, int WAVES, int BN, int OCC, bool ALIGNED>
+template <typename T, int DP, int WAVES, int BN, int OCC, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   using L = Tile<T, DP>;
-  constexpr int NT = DP / 16, NB = DP / 32, KB = BN / 32, BM = 32 * QB * WAVES;
+  constexpr int NT = DP / 16, NB = DP / 32, KB = BN / 32, BM = 32 * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int32_t cu_lds[kCuLds];
   constexpr int TILE = BN * L::kRowBytes;
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   const int t = ranked_tile(tiles, blockIdx.x / a.Hq, [&](int x) { return min((x + 1) * BM, a.N) - find_seq(cu, a.S, x * BM, a.N).start; });
   const int h = xcd_swizzle(blockIdx.x % a.Hq, a.Hq), kv = h / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
-  const int i0 = t * BM, w0 = i0 + wave_id() * 32 * QB;
+  const int i0 = t * BM, w0 = i0 + wave_id() * 32;
   const T *Kb = a.K + int64_t(kv) * a.D, *Vb = a.V + int64_t(kv) * a.D;
 
   const int kmin = __builtin_amdgcn_readfirstlane(find_seq(cu, a.S, i0, a.N).start);
@@ -443,45 +443,34 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   const Stager<T, DP, BN, WAVES, ALIGNED> stage_k(a.ldk, a.D), stage_v(a.ldv, a.D);
   stage_k(k_tile(0), Kb, kmin, a.N);
 
-  Operand<T> q[QB][NT];
-  Seq seq[QB];
+  Operand<T> q[NT];
+  const int i = w0 + col;
+  const Seq seq = find_seq(cu, a.S, i, a.N);
+  const T* qr = a.Q + int64_t(min(i, a.N - 1)) * a.ldq + int64_t(h) * a.D;
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const int i = w0 + 32 * b + col;
-    seq[b] = find_seq(cu, a.S, i, a.N);
-    const T* row = a.Q + int64_t(min(i, a.N - 1)) * a.ldq + int64_t(h) * a.D;
-#pragma unroll
-    for (int s = 0; s < NT; ++s) q[b][s] = load_row<T, ALIGNED>(row, 16 * s + 8 * hi, a.D);
-  }
+  for (int u = 0; u < NT; ++u) q[u] = load_row<T, ALIGNED>(qr, 16 * u + 8 * hi, a.D);
   // the wave's tiles nb .. ne - 1, from its first row's start to its last row; all of its
   // rows see a tile that begins at or behind the last row's start and ends at or before
   // the first row
-  const int nb = min((max(__builtin_amdgcn_readfirstlane(seq[0].start), kmin) - kmin) / BN, turns);  // rows beyond N: none
-  const int ne = min((w0 + 32 * QB - kmin + BN - 1) / BN, turns);
-  const int lastStart = __builtin_amdgcn_readlane(seq[QB - 1].start, 31);
+  const int nb = min((max(__builtin_amdgcn_readfirstlane(seq.start), kmin) - kmin) / BN, turns);  // rows beyond N: none
+  const int ne = min((w0 + 32 - kmin + BN - 1) / BN, turns);
+  const int lastStart = __builtin_amdgcn_readlane(seq.start, 31);
 
-  f32x16 o[QB][NB];
-  float m[QB], l[QB];
+  f32x16 o[NB];
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    m[b] = -INFINITY;
-    l[b] = 0.f;
-#pragma unroll
-    for (int d = 0; d < NB; ++d) o[b][d] = zero16();
-  }
+  for (int d = 0; d < NB; ++d) o[d] = zero16();
   const float c = a.scale * kLog2e, slack = 8.f / c;
 
-  f32x16 s[QB][KB];        // scores of a tile, then its weights
-  Operand<T> p[QB][KB][2];  // the weights as operands
-  float mc[QB];
+  f32x16 s[KB];         // scores of a tile, then its weights
+  Operand<T> p[KB][2];  // the weights as operands
+  float mc;
   const auto scores = [&](int x, const char* kt) {
-#pragma unroll
-    for (int b = 0; b < QB; ++b) s[b][x] = zero16();
+    s[x] = zero16();
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const Operand<T> k = L::by_rows(kt, 32 * x, u);
-#pragma unroll
-      for (int b = 0; b < QB; ++b) s[b][x] = mma(k, q[b][u], s[b][x]);
+      s[x] = mma(k, q[u], s[x]);
     }
   };
   const auto values = [&](const char* vt) {
@@ -492,57 +481,45 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
 #pragma unroll
         for (int d = 0; d < NB; ++d) {
           const Operand<T> v = L::by_cols(vt, 32 * x + 16 * u, d);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) o[b][d] = mma(v, p[b][x][u], o[b][d]);
+          o[d] = mma(v, p[x][u], o[d]);
         }
   };
   const auto mask = [&](int k0) {
+    // start <= j <= i in one comparison
+    const uint32_t most = i - seq.start, at = k0 + 4 * hi - seq.start;
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      // start <= j <= i in one comparison
-      const uint32_t most = w0 + 32 * b + col - seq[b].start, at = k0 + 4 * hi - seq[b].start;
+    for (int x = 0; x < KB; ++x)
 #pragma unroll
-      for (int x = 0; x < KB; ++x)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) s[b][x][v] = at + (32 * x + mfma32_row(v, 0)) <= most ? s[b][x][v] : -INFINITY;
-    }
+      for (int v = 0; v < 16; ++v) s[x][v] = at + (32 * x + mfma32_row(v, 0)) <= most ? s[x][v] : -INFINITY;
   };
   // The reference m of a row's weights exp(s - m) stays until a score passes it by 2^8:
   // weights up to 2^8 lose nothing in a float, and the sums are seldom scaled (by f).
-  const auto reference = [&](float (&f)[QB]) {
+  const auto reference = [&] {
+    float top = s[0][0];
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      float top = s[b][0][0];
+    for (int x = 0; x < KB; ++x)
 #pragma unroll
-      for (int x = 0; x < KB; ++x)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) top = fmaxf(top, s[b][x][v]);
-      top = join_halves(top, max2);
-      const float mn = top > m[b] + slack ? top : m[b];
-      f[b] = m[b] == mn ? 1.f : __builtin_amdgcn_exp2f((m[b] - mn) * c);
-      l[b] *= f[b];
-      m[b] = mn;
-      mc[b] = mn == -INFINITY ? 0.f : mn * c;
-    }
+      for (int v = 0; v < 16; ++v) top = fmaxf(top, s[x][v]);
+    top = join_halves(top, max2);
+    const float mn = top > m + slack ? top : m;
+    const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
+    l *= f;
+    m = mn;
+    mc = mn == -INFINITY ? 0.f : mn * c;
+    return f;
   };
   const auto weights = [&](int x) {
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        s[b][x][v] = __builtin_amdgcn_exp2f(fmaf(s[b][x][v], c, -mc[b]));
-        sum[v & 1] += s[b][x][v];
-      }
-      l[b] += sum[0] + sum[1];
+    for (int v = 0; v < 16; ++v) {
+      s[x][v] = __builtin_amdgcn_exp2f(fmaf(s[x][v], c, -mc));
+      sum[v & 1] += s[x][v];
     }
+    l += sum[0] + sum[1];
   };
   const auto operands = [&](int x) {
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      p[b][x][0] = as_operand<T>(s[b][x], 0);
-      p[b][x][1] = as_operand<T>(s[b][x], 1);
-    }
+    p[x][0] = as_operand<T>(s[x], 0);
+    p[x][1] = as_operand<T>(s[x], 1);
   };
   const auto begin = [&](int n) {  // a turn's wait and copies
     wait_vmcnt<0>();
@@ -562,24 +539,22 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
     begin(n);
     const int k0 = kmin + n * BN;
     if (!(k0 + BN - 1 <= w0 && k0 >= lastStart)) mask(k0);
-    float f[QB];
+    float f;
     if (n > nb) {
       const char* vt = v_tile((n + 1) & 1);
       values(vt);
-      reference(f);
+      f = reference();
       weights(0);
     } else {
-      reference(f);
+      f = reference();
       weights(0);
     }
+    if (__any(f != 1.f)) {
 #pragma unroll
-    for (int b = 0; b < QB; ++b)
-      if (__any(f[b] != 1.f)) {
+      for (int d = 0; d < NB; ++d)
 #pragma unroll
-        for (int d = 0; d < NB; ++d)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) o[b][d][v] *= f[b];
-      }
+        for (int v = 0; v < 16; ++v) o[d][v] *= f;
+    }
     // behind the wave's last tile the next scores are of no use
     const char* kt = k_tile((n + 1) & 1);
 #pragma unroll
@@ -593,25 +568,20 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   values(v_tile((n + 1) & 1));
   for (++n; n <= turns; ++n) begin(n);
 
+  const bool in = seq.inside;
+  const float sum = join_halves(l, sum2), inv = 1.f / sum;
+  T* row = a.out + int64_t(min(i, a.N - 1)) * a.ldo + int64_t(h) * a.D;
+  if (in) {
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const int i = w0 + 32 * b + col;
-    const bool in = seq[b].inside;
-    const float sum = join_halves(l[b], sum2), inv = 1.f / sum;
-    T* row = a.out + int64_t(min(i, a.N - 1)) * a.ldo + int64_t(h) * a.D;
-    if (in) {
-#pragma unroll
-      for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, o[b][d], inv);
-      if (hi == 0) a.lse[int64_t(h) * a.N + i] = (m[b] * c + __builtin_amdgcn_logf(sum)) * kLn2;
-    }
-    // a NaN of the sum is one of a weight, and in every column
-    const bool lost = sum != sum || far(m[b], c);
-    if (any_bad<true>(o[b], in) || __any(in && lost)) {
-      for (int r = 0; r < 32; ++r)
-        if (__builtin_amdgcn_readlane(int(in), r))
-          fwd_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r),
-                  __builtin_amdgcn_readlane(int(lost), r));
-    }
+    for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, o[d], inv);
+    if (hi == 0) a.lse[int64_t(h) * a.N + i] = (m * c + __builtin_amdgcn_logf(sum)) * kLn2;
+  }
+  // a NaN of the sum is one of a weight, and in every column
+  const bool lost = sum != sum || far(m, c);
+  if (any_bad<true>(o, in) || __any(in && lost)) {
+    for (int r = 0; r < 32; ++r)
+      if (__builtin_amdgcn_readlane(int(in), r))
+        fwd_row(a, h, kv, w0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(lost), r));
   }
 }
 
@@ -619,7 +589,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
 // 32 WAVES keys each, with a softmax of their own; their sums are joined at the end.  Bound by
 // the latency of one block's turns, a copy and two short products each: all of a tile's
 // keys at a time make a quarter as many.  128 rows of 4 x 64 fp32 in one sequence: 7.8 us.
-template <typename T, int DP, int WAVES, int BUFS, bool ALIGNED>
+template <typename T, int DP, int WAVES, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   using L = Tile<T, DP>;
   constexpr int NT = DP / 16, NB = DP / 32, BN = 32 * WAVES;
@@ -627,8 +597,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   __shared__ int32_t cu_lds[kCuLds];
   __shared__ float ms[WAVES][2][32];  // of each wave: reference and sum
   constexpr int TILE = BN * L::kRowBytes;
-  const auto k_tile = [&](int n) { return smem + (n % BUFS) * 2 * TILE; };
-  const auto v_tile = [&](int n) { return smem + (n % BUFS) * 2 * TILE + TILE; };
+  char *const kt = smem, *const vt = smem + TILE;
 
   const int t = (a.N + 31) / 32 - 1 - blockIdx.x / a.Hq;
   const int h = xcd_swizzle(blockIdx.x % a.Hq, a.Hq), kv = h / (a.Hq / a.Hkv);
@@ -641,8 +610,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   const int turns = (min(i0 + 32, a.N) - kmin + BN - 1) / BN;
   const Stager<T, DP, BN, WAVES, ALIGNED> stage_k(a.ldk, a.D), stage_v(a.ldv, a.D);
   const auto stage = [&](int n) {
-    stage_k(k_tile(n), Kb, kmin + n * BN, a.N);
-    stage_v(v_tile(n), Vb, kmin + n * BN, a.N);
+    stage_k(kt, Kb, kmin + n * BN, a.N);
+    stage_v(vt, Vb, kmin + n * BN, a.N);
   };
   stage(0);
   Operand<T> q[NT];
@@ -657,10 +626,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   for (int n = 0; n < turns; ++n) {
     wait_vmcnt<0>();
     __syncthreads();
-    if (BUFS > 1 && n + 1 < turns) stage(n + 1);
     const int k0 = kmin + n * BN + 32 * w;
     if (k0 < i0 + 32) {
-      const char *kt = k_tile(n), *vt = v_tile(n);
       f32x16 s = zero16();
 #pragma unroll
       for (int u = 0; u < NT; ++u) s = mma(L::by_rows(kt, 32 * w, u), q[u], s);
@@ -688,14 +655,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
         for (int u = 0; u < 2; ++u) o[d] = mma(L::by_cols(vt, 32 * w + 16 * u, d), as_operand<T>(s, u), o[d]);
       }
     }
-    if (BUFS == 1 && n + 1 < turns) {
+    if (n + 1 < turns) {
       __syncthreads();
       stage(n + 1);
     }
   }
   __syncthreads();
   float* part = reinterpret_cast<float*>(smem);  // [WAVES][DP][32]
-  static_assert(WAVES * DP * 32 * 4 <= BUFS * 2 * TILE, "the tiles' room");
+  static_assert(WAVES * DP * 32 * 4 <= 2 * TILE, "the tiles' room");
 #pragma unroll
   for (int d = 0; d < NB; ++d)
 #pragma unroll
@@ -768,10 +735,10 @@ __device__ __forceinline__ void dq_row(const AttnArgs<T>& a, int h, int kv, int 
 // bf16: 16384 rows of 16 x 64 in sequences of 1 to 4099 171 us (753 TFLOP/s); 8192 of 16 x 128 in
 // sequences of 2048 130 us (793).
 // Bound by issue as the forward pass, with 4 vector operations a score.
-template <typename T, int DP, int QB, int WAVES, int BN, int OCC, bool ALIGNED>
+template <typename T, int DP, int WAVES, int BN, int OCC, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
   using L = Tile<T, DP>;
-  constexpr int NT = DP / 16, NB = DP / 32, KB = BN / 32, BM = 32 * QB * WAVES;
+  constexpr int NT = DP / 16, NB = DP / 32, KB = BN / 32, BM = 32 * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int32_t cu_lds[kCuLds];
   constexpr int TILE = BN * L::kRowBytes;
@@ -784,7 +751,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
   const int t = ranked_tile(tiles, blockIdx.x / heads, [&](int x) { return min((x + 1) * BM, a.N) - find_seq(cu, a.S, x * BM, a.N).start; });
   const int sp = blockIdx.x % heads / a.Hq, h = xcd_swizzle(blockIdx.x % a.Hq, a.Hq), kv = h / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
-  const int i0 = t * BM, w0 = i0 + wave_id() * 32 * QB;
+  const int i0 = t * BM, w0 = i0 + wave_id() * 32;
   const T *Kb = a.K + int64_t(kv) * a.D, *Vb = a.V + int64_t(kv) * a.D;
 
   // the split's tiles: sp, sp + splits, ... of the block's range
@@ -798,40 +765,32 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
   };
   if (turns > 0) stage(0);
 
-  Operand<T> q[QB][NT], go[QB][NT];
-  Seq seq[QB];
-  float delta[QB], lse2[QB];
+  Operand<T> q[NT], go[NT];
+  const int i = w0 + col;
+  const int64_t r = min(i, a.N - 1);
+  const Seq seq = find_seq(cu, a.S, i, a.N);
+  const T *qr = a.Q + r * a.ldq + int64_t(h) * a.D, *gr = a.gO + r * a.ldgo + int64_t(h) * a.D;
+  const T* orow = a.O + r * a.ldo + int64_t(h) * a.D;
+  float s = 0.f;
 #pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const int i = w0 + 32 * b + col;
-    const int64_t r = min(i, a.N - 1);
-    seq[b] = find_seq(cu, a.S, i, a.N);
-    const T *qr = a.Q + r * a.ldq + int64_t(h) * a.D, *gr = a.gO + r * a.ldgo + int64_t(h) * a.D;
-    const T* orow = a.O + r * a.ldo + int64_t(h) * a.D;
-    float s = 0.f;
+  for (int u = 0; u < NT; ++u) {
+    q[u] = load_row<T, ALIGNED>(qr, 16 * u + 8 * hi, a.D);
+    go[u] = load_row<T, ALIGNED>(gr, 16 * u + 8 * hi, a.D);
+    const Operand<T> x = load_row<T, ALIGNED>(orow, 16 * u + 8 * hi, a.D);
 #pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      q[b][u] = load_row<T, ALIGNED>(qr, 16 * u + 8 * hi, a.D);
-      go[b][u] = load_row<T, ALIGNED>(gr, 16 * u + 8 * hi, a.D);
-      const Operand<T> x = load_row<T, ALIGNED>(orow, 16 * u + 8 * hi, a.D);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(static_cast<float>(go[b][u].v[e]), static_cast<float>(x.v[e]), s);
-    }
-    delta[b] = join_halves(s, sum2);
-    lse2[b] = a.lse[int64_t(h) * a.N + r] * kLog2e;
-    if (sp == 0 && hi == 0 && i < a.N) {
-      a.rows[int64_t(2 * h) * a.N + i] = seq[b].inside ? -a.lse[int64_t(h) * a.N + i] / a.scale : 0.f;
-      a.rows[int64_t(2 * h + 1) * a.N + i] = seq[b].inside ? -delta[b] : 0.f;
-    }
+    for (int e = 0; e < 8; ++e) s = fmaf(static_cast<float>(go[u].v[e]), static_cast<float>(x.v[e]), s);
   }
-  const int first = __builtin_amdgcn_readfirstlane(seq[0].start);
-  const int lastStart = __builtin_amdgcn_readlane(seq[QB - 1].start, 31);
+  const float delta = join_halves(s, sum2), lse2 = a.lse[int64_t(h) * a.N + r] * kLog2e;
+  if (sp == 0 && hi == 0 && i < a.N) {
+    a.rows[int64_t(2 * h) * a.N + i] = seq.inside ? -a.lse[int64_t(h) * a.N + i] / a.scale : 0.f;
+    a.rows[int64_t(2 * h + 1) * a.N + i] = seq.inside ? -delta : 0.f;
+  }
+  const int first = __builtin_amdgcn_readfirstlane(seq.start);
+  const int lastStart = __builtin_amdgcn_readlane(seq.start, 31);
 
-  f32x16 g[QB][NB];
+  f32x16 g[NB];
 #pragma unroll
-  for (int b = 0; b < QB; ++b)
-#pragma unroll
-    for (int d = 0; d < NB; ++d) g[b][d] = zero16();
+  for (int d = 0; d < NB; ++d) g[d] = zero16();
   const float c = a.scale * kLog2e;
 
   for (int n = 0; n < turns; ++n) {
@@ -839,71 +798,56 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
     __syncthreads();
     if (n + 1 < turns) stage(n + 1);
     const int k0 = kmin + n * step;
-    if (k0 + BN <= first || k0 >= w0 + 32 * QB) continue;
+    if (k0 + BN <= first || k0 >= w0 + 32) continue;
     const bool whole = k0 + BN - 1 <= w0 && k0 >= lastStart;
     const char *kt = k_tile(n & 1), *vt = v_tile(n & 1);
 #pragma unroll
     for (int x = 0; x < KB; ++x) {
-      f32x16 s[QB], dp[QB];
-#pragma unroll
-      for (int b = 0; b < QB; ++b) s[b] = dp[b] = zero16();
+      f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         const Operand<T> k = L::by_rows(kt, 32 * x, u), v = L::by_rows(vt, 32 * x, u);
-#pragma unroll
-        for (int b = 0; b < QB; ++b) {
-          s[b] = mma(k, q[b][u], s[b]);
-          dp[b] = mma(v, go[b][u], dp[b]);
-        }
+        s = mma(k, q[u], s);
+        dp = mma(v, go[u], dp);
       }
-      Operand<T> ds[QB][2];
 #pragma unroll
-      for (int b = 0; b < QB; ++b) {
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[b][v], c, -lse2[b]));
-          s[b][v] = p * (dp[b][v] - delta[b]);
-        }
-        if (!whole) {
-          const uint32_t most = w0 + 32 * b + col - seq[b].start, at = k0 + 32 * x + 4 * hi - seq[b].start;
-#pragma unroll
-          for (int v = 0; v < 16; ++v) s[b][v] = at + mfma32_row(v, 0) <= most ? s[b][v] : 0.f;
-        }
-        ds[b][0] = as_operand<T>(s[b], 0);
-        ds[b][1] = as_operand<T>(s[b], 1);
+      for (int v = 0; v < 16; ++v) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[v], c, -lse2));
+        s[v] = p * (dp[v] - delta);
       }
+      if (!whole) {
+        const uint32_t most = i - seq.start, at = k0 + 32 * x + 4 * hi - seq.start;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[v] = at + mfma32_row(v, 0) <= most ? s[v] : 0.f;
+      }
+      const Operand<T> ds[2] = {as_operand<T>(s, 0), as_operand<T>(s, 1)};
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int d = 0; d < NB; ++d) {
           const Operand<T> k = L::by_cols(kt, 32 * x + 16 * u, d);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) g[b][d] = mma(k, ds[b][u], g[b][d]);
+          g[d] = mma(k, ds[u], g[d]);
         }
     }
   }
 
-#pragma unroll
-  for (int b = 0; b < QB; ++b) {
-    const int i = w0 + 32 * b + col;
-    const bool in = seq[b].inside;
-    if (a.splits > 1) {
-      float* row = a.part + ((int64_t(sp) * a.N + min(i, a.N - 1)) * a.Hq + h) * a.D;
-      if (in) {
-#pragma unroll
-        for (int d = 0; d < NB; ++d) put_block<float, ALIGNED>(row, d, a.D, g[b][d], a.scale);
-      }
-      continue;
-    }
-    T* row = a.gQ + int64_t(min(i, a.N - 1)) * a.ldgq + int64_t(h) * a.D;
+  const bool in = seq.inside;
+  if (a.splits > 1) {
+    float* row = a.part + ((int64_t(sp) * a.N + r) * a.Hq + h) * a.D;
     if (in) {
 #pragma unroll
-      for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, g[b][d], a.scale);
+      for (int d = 0; d < NB; ++d) put_block<float, ALIGNED>(row, d, a.D, g[d], a.scale);
     }
-    if (any_bad<false>(g[b], in)) {
-      for (int r = 0; r < 32; ++r)
-        if (__builtin_amdgcn_readlane(int(in), r)) dq_row(a, h, kv, w0 + 32 * b + r, __builtin_amdgcn_readlane(seq[b].start, r));
-    }
+    return;
+  }
+  T* row = a.gQ + r * a.ldgq + int64_t(h) * a.D;
+  if (in) {
+#pragma unroll
+    for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, g[d], a.scale);
+  }
+  if (any_bad<false>(g, in)) {
+    for (int r = 0; r < 32; ++r)
+      if (__builtin_amdgcn_readlane(int(in), r)) dq_row(a, h, kv, w0 + r, __builtin_amdgcn_readlane(seq.start, r));
   }
 }
 
@@ -944,10 +888,10 @@ __device__ __forceinline__ void dkv_row(const AttnArgs<T>& a, int kv, int j, int
 template <typename T, int DP>
 constexpr bool v_in_lds = sizeof(T) == 2 && DP > 96;
 
-template <typename T, int DP, int KB, int WAVES, int BN, int OCC, bool ALIGNED>
+template <typename T, int DP, int WAVES, int BN, int OCC, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   using L = Tile<T, DP>;
-  constexpr int NT = DP / 16, NB = DP / 32, QB = BN / 32, BM = 32 * KB * WAVES;
+  constexpr int NT = DP / 16, NB = DP / 32, QB = BN / 32, BM = 32 * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int32_t cu_lds[kCuLds];
   __shared__ __attribute__((aligned(16))) float stats[2][2][BN];  // of the tile's rows: -lse / scale and -delta
@@ -964,7 +908,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   const int sp = blockIdx.x % heads / a.Hkv, kv = xcd_swizzle(blockIdx.x % a.Hkv, a.Hkv);
   const int G = a.Hq / a.Hkv;
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
-  const int j0 = t * BM, w0 = j0 + wave_id() * 32 * KB;
+  const int j0 = t * BM, w0 = j0 + wave_id() * 32;
 
   const int last = min(j0 + BM, a.N) - 1;
   const int qmax = __builtin_amdgcn_readfirstlane(find_seq(cu, a.S, last, a.N).end);
@@ -986,28 +930,22 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
   if constexpr (VL)  // through registers, which puts zeros behind column D: gO's tile has none there
     Stager<T, DP, BM, WAVES, false>(a.ldv, a.D)(vl, a.V + int64_t(kv) * a.D, j0, a.N);
 
-  Operand<T> k[KB][NT], v[KB][VL ? 1 : NT];
-  Seq seq[KB];
+  Operand<T> k[NT], v[VL ? 1 : NT];
+  const int j = w0 + col;
+  const int64_t r = min(j, a.N - 1);
+  const Seq seq = find_seq(cu, a.S, j, a.N);
+  const T *kr = a.K + r * a.ldk + int64_t(kv) * a.D, *vr = a.V + r * a.ldv + int64_t(kv) * a.D;
 #pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    const int j = w0 + 32 * b + col;
-    const int64_t r = min(j, a.N - 1);
-    seq[b] = find_seq(cu, a.S, j, a.N);
-    const T *kr = a.K + r * a.ldk + int64_t(kv) * a.D, *vr = a.V + r * a.ldv + int64_t(kv) * a.D;
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      k[b][u] = load_row<T, ALIGNED>(kr, 16 * u + 8 * hi, a.D);
-      if constexpr (!VL) v[b][u] = load_row<T, ALIGNED>(vr, 16 * u + 8 * hi, a.D);
-    }
+  for (int u = 0; u < NT; ++u) {
+    k[u] = load_row<T, ALIGNED>(kr, 16 * u + 8 * hi, a.D);
+    if constexpr (!VL) v[u] = load_row<T, ALIGNED>(vr, 16 * u + 8 * hi, a.D);
   }
-  const int firstEnd = __builtin_amdgcn_readfirstlane(seq[0].end);
-  const int lastEnd = __builtin_amdgcn_readlane(seq[KB - 1].end, 31);
+  const int firstEnd = __builtin_amdgcn_readfirstlane(seq.end);
+  const int lastEnd = __builtin_amdgcn_readlane(seq.end, 31);
 
-  f32x16 gk[KB][NB], gv[KB][NB];
+  f32x16 gk[NB], gv[NB];
 #pragma unroll
-  for (int b = 0; b < KB; ++b)
-#pragma unroll
-    for (int d = 0; d < NB; ++d) gk[b][d] = gv[b][d] = zero16();
+  for (int d = 0; d < NB; ++d) gk[d] = gv[d] = zero16();
   const float c = a.scale * kLog2e;
 
   for (int n = 0; n < turns; ++n) {
@@ -1016,11 +954,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
     if (n + 1 < turns) stage(n + 1);
     const int i0 = j0 + (sp + n * a.splits) % per * BN;
     if (i0 + BN <= w0 || i0 >= lastEnd) continue;
-    const bool whole = i0 >= w0 + 32 * KB - 1 && i0 + BN <= firstEnd;
+    const bool whole = i0 >= w0 + 31 && i0 + BN <= firstEnd;
     const char *qt = q_tile(n & 1), *gt = g_tile(n & 1);
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
-      f32x16 s[KB], dp[KB];
       // the sums begin at the rows' -lse / scale and -delta, so that exp(scale s) is the weight
       // and the other the difference; fp32 adds the log-sum last, to lose nothing beside it
       f32x16 y, z;
@@ -1035,92 +972,74 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
         }
       }
       constexpr bool LATE = sizeof(T) == 4;
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        s[b] = LATE ? zero16() : y;
-        dp[b] = z;
-      }
+      f32x16 s = LATE ? zero16() : y, dp = z;
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         const Operand<T> q = L::by_rows(qt, 32 * x, u), go = L::by_rows(gt, 32 * x, u);
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          s[b] = mma(q, k[b][u], s[b]);
-          if constexpr (VL)
-            dp[b] = mma(go, L::by_rows(vl, 32 * (KB * wave_id() + b), u), dp[b]);
-          else
-            dp[b] = mma(go, v[b][u], dp[b]);
-        }
+        s = mma(q, k[u], s);
+        if constexpr (VL)
+          dp = mma(go, L::by_rows(vl, 32 * wave_id(), u), dp);
+        else
+          dp = mma(go, v[u], dp);
       }
-      Operand<T> p[KB][2], ds[KB][2];
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const int j = w0 + 32 * b + col;
+      for (int r = 0; r < 16; ++r) {
+        s[r] = __builtin_amdgcn_exp2f((LATE ? s[r] + y[r] : s[r]) * c);
+        dp[r] *= s[r];
+      }
+      if (!whole) {
+        // j <= i < end in one comparison
+        const uint32_t most = seq.end - j, at = i0 + 32 * x + 4 * hi - j;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          s[b][r] = __builtin_amdgcn_exp2f((LATE ? s[b][r] + y[r] : s[b][r]) * c);
-          dp[b][r] *= s[b][r];
+          const bool seen = at + mfma32_row(r, 0) < most;
+          s[r] = seen ? s[r] : 0.f;
+          dp[r] = seen ? dp[r] : 0.f;
         }
-        if (!whole) {
-          // j <= i < end in one comparison
-          const uint32_t most = seq[b].end - j, at = i0 + 32 * x + 4 * hi - j;
+      }
+      Operand<T> p[2], ds[2];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const bool seen = at + mfma32_row(r, 0) < most;
-            s[b][r] = seen ? s[b][r] : 0.f;
-            dp[b][r] = seen ? dp[b][r] : 0.f;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          p[b][u] = as_operand<T>(s[b], u);
-          ds[b][u] = as_operand<T>(dp[b], u);
-        }
+      for (int u = 0; u < 2; ++u) {
+        p[u] = as_operand<T>(s, u);
+        ds[u] = as_operand<T>(dp, u);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int d = 0; d < NB; ++d) {
           const Operand<T> go = L::by_cols(gt, 32 * x + 16 * u, d), q = L::by_cols(qt, 32 * x + 16 * u, d);
-#pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            gv[b][d] = mma(go, p[b][u], gv[b][d]);
-            gk[b][d] = mma(q, ds[b][u], gk[b][d]);
-          }
+          gv[d] = mma(go, p[u], gv[d]);
+          gk[d] = mma(q, ds[u], gk[d]);
         }
     }
   }
 
+  const bool in = seq.inside;
 #pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    const int j = w0 + 32 * b + col;
-    const bool in = seq[b].inside;
+  for (int y = 0; y < 2; ++y) {  // gK, then gV
+    const f32x16(&g)[NB] = y == 0 ? gk : gv;
+    const float f = y == 0 ? a.scale : 1.f;
     if (a.splits > 1) {
-      float* row = a.part + ((int64_t(sp) * a.N + min(j, a.N - 1)) * 2 * a.Hkv + kv) * a.D;
+      float* row = a.part + (((int64_t(sp) * a.N + r) * 2 + y) * a.Hkv + kv) * a.D;
       if (in) {
 #pragma unroll
-        for (int d = 0; d < NB; ++d) {
-          put_block<float, ALIGNED>(row, d, a.D, gk[b][d], a.scale);
-          put_block<float, ALIGNED>(row + int64_t(a.Hkv) * a.D, d, a.D, gv[b][d], 1.f);
-        }
+        for (int d = 0; d < NB; ++d) put_block<float, ALIGNED>(row, d, a.D, g[d], f);
       }
       continue;
     }
-    T* kr = a.gK + int64_t(min(j, a.N - 1)) * a.ldgk + int64_t(kv) * a.D;
-    T* vr = a.gV + int64_t(min(j, a.N - 1)) * a.ldgv + int64_t(kv) * a.D;
+    T* row = (y == 0 ? a.gK + r * a.ldgk : a.gV + r * a.ldgv) + int64_t(kv) * a.D;
     if (in) {
 #pragma unroll
-      for (int d = 0; d < NB; ++d) {
-        put_block<T, ALIGNED>(kr, d, a.D, gk[b][d], a.scale);
-        put_block<T, ALIGNED>(vr, d, a.D, gv[b][d], 1.f);
-      }
+      for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, g[d], f);
     }
-    const bool bad_k = any_bad<false>(gk[b], in), bad_v = any_bad<false>(gv[b], in);
-    for (int r = 0; (bad_k || bad_v) && r < 32; ++r) {
-      if (!__builtin_amdgcn_readlane(int(in), r)) continue;
-      const int end = __builtin_amdgcn_readlane(seq[b].end, r);
-      if (bad_k) dkv_row<false>(a, kv, w0 + 32 * b + r, end);
-      if (bad_v) dkv_row<true>(a, kv, w0 + 32 * b + r, end);
+    if (!any_bad<false>(g, in)) continue;
+    for (int x = 0; x < 32; ++x) {
+      if (!__builtin_amdgcn_readlane(int(in), x)) continue;
+      const int end = __builtin_amdgcn_readlane(seq.end, x);
+      if (y == 0)
+        dkv_row<false>(a, kv, w0 + x, end);
+      else
+        dkv_row<true>(a, kv, w0 + x, end);
     }
   }
 }
@@ -1204,10 +1123,10 @@ template <typename T, int DP, bool ALIGNED>
 void fwd_t(const AttnArgs<T>& a, hipStream_t s) {
   const int64_t blocks = row_blocks(a.N, a.Hq);
   if (blocks < 256)
-    return go<k_attn_fwd_few<T, DP, kWaves, 1, ALIGNED>, 2 * kRows * Tile<T, DP>::kRowBytes>(
+    return go<k_attn_fwd_few<T, DP, kWaves, ALIGNED>, 2 * kRows * Tile<T, DP>::kRowBytes>(
         a, (int64_t(a.N) + 31) / 32 * a.Hq, kWaves, s);
   constexpr int BN = sizeof(T) == 2 ? 64 : 32, OCC = sizeof(T) == 2 ? 2 : 1;
-  go<k_attn_fwd<T, DP, 1, kWaves, BN, OCC, ALIGNED>, kLds<T, DP, BN>>(a, blocks, kWaves, s);
+  go<k_attn_fwd<T, DP, kWaves, BN, OCC, ALIGNED>, kLds<T, DP, BN>>(a, blocks, kWaves, s);
 }
 
 // Backward with few blocks: the range of a block is split over several, and their sums
@@ -1229,7 +1148,7 @@ void bwd_t(AttnArgs<T> a, hipStream_t s) {
   constexpr bool B = sizeof(T) == 2;
   constexpr int OCC = B ? 2 : 1, BQ = B ? 64 : 32, BK = B && DP <= 96 ? 64 : 32;
   a.splits = dq_splits(a.N, a.Hq);
-  go<k_attn_dq<T, DP, 1, kWaves, BQ, OCC, ALIGNED>, kLds<T, DP, BQ>>(a, row_blocks(a.N, a.Hq) * a.splits, kWaves, s);
+  go<k_attn_dq<T, DP, kWaves, BQ, OCC, ALIGNED>, kLds<T, DP, BQ>>(a, row_blocks(a.N, a.Hq) * a.splits, kWaves, s);
   const auto join = [&](int keys) {
     if (a.splits == 1) return;
     if (a.N >= 8192)
@@ -1240,7 +1159,7 @@ void bwd_t(AttnArgs<T> a, hipStream_t s) {
   join(0);
   a.splits = dkv_splits(a.N, a.Hkv);
   constexpr int VL = v_in_lds<T, DP> ? kRows * Tile<T, DP>::kRowBytes : 0;
-  go<k_attn_dkv<T, DP, 1, kWaves, BK, OCC, ALIGNED>, kLds<T, DP, BK> + VL>(a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
+  go<k_attn_dkv<T, DP, kWaves, BK, OCC, ALIGNED>, kLds<T, DP, BK> + VL>(a, row_blocks(a.N, a.Hkv) * a.splits, kWaves, s);
   join(1);
 }
 
