@@ -574,7 +574,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   if (in) {
 #pragma unroll
     for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, o[d], inv);
-    if (hi == 0) a.lse[int64_t(h) * a.N + i] = (m * c + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (hi == 0) a.lse[int64_t(h) * a.N + i] = fmaf(m, c, __builtin_amdgcn_logf(sum)) * kLn2;
   }
   // a NaN of the sum is one of a weight, and in every column
   const bool lost = sum != sum || far(m, c);
@@ -702,7 +702,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
     }
     if (seq.inside) put4<T, ALIGNED>(row, c0 + e, a.D, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
   }
-  if (seq.inside && hi == 0 && w == 0) a.lse[int64_t(h) * a.N + i] = (m * c + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (seq.inside && hi == 0 && w == 0) a.lse[int64_t(h) * a.N + i] = fmaf(m, c, __builtin_amdgcn_logf(sum)) * kLn2;
   const bool lost = sum != sum || far(m, c);
   if (__syncthreads_or(seq.inside && (bad || lost))) {
     for (int r = w; r < 32; r += WAVES)
