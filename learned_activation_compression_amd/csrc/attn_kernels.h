@@ -21,8 +21,9 @@
 // A row outside the sequences, or beyond N, is read at a row that exists; its
 // products are masked or not stored.  A masked product is replaced before the
 // softmax, but a zero weight times an infinity or NaN in a masked place would still
-// spoil a sum of products: an output block that holds a NaN is computed again, row by
-// row over its visible rows alone.  So are rows with an infinity in a product's padding:
+// spoil a sum of products: rows of an output block that holds a NaN are computed again, one
+// by one over their visible rows alone (in the forward pass those whose NaN no value that
+// they see explains).  So are rows with an infinity in a product's padding:
 // behind its D columns an aligned tile repeats a row's first ones, which meet zeros of the
 // other side.  That makes a NaN of a score, and of everything that it enters, so a
 // log-sum that is NaN is formed again as well.  And so are rows of very large scores (far)
@@ -333,14 +334,13 @@ __device__ __forceinline__ void put_block(T* row, int db, int D, const f32x16& x
     put4<T, ALIGNED>(row, 32 * db + 8 * g + 4 * h, D, x[4 * g] * f, x[4 * g + 1] * f, x[4 * g + 2] * f, x[4 * g + 3] * f);
 }
 
-// of the lanes `in`; FINITE: infinities too
-template <bool FINITE, int NB>
-__device__ __forceinline__ bool any_bad(const f32x16 (&x)[NB], bool in) {
+template <int NB>
+__device__ __forceinline__ bool any_nan(const f32x16 (&x)[NB], bool in) {
   bool bad = false;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) bad = bad || (FINITE ? !(fabsf(x[b][v]) < INFINITY) : x[b][v] != x[b][v]);
+    for (int v = 0; v < 16; ++v) bad = bad || x[b][v] != x[b][v];
   return __any(in && bad);
 }
 
@@ -376,6 +376,43 @@ struct LaneSum {
     if (l + 64 < D) row[l + 64] = from_f32<T>(b * f);
   }
 };
+
+// Of the columns l and l + 64 of the rows from .. to: the last that holds a NaN, and the last
+// that holds an infinity (-1: none).
+struct Spoilt {
+  int nan[2] = {-1, -1}, inf[2] = {-1, -1};
+};
+template <typename T>
+__device__ __forceinline__ Spoilt last_spoilt(const T* x, int64_t ld, int from, int to, int D) {
+  const int l = threadIdx.x & 63, col[2] = {min(l, D - 1), min(l + 64, D - 1)};
+  Spoilt s;
+  constexpr int AHEAD = 16;
+  for (int j = to; j >= from && !__all(s.nan[0] >= 0 && s.nan[1] >= 0); j -= AHEAD) {
+    T y[AHEAD][2];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) y[u][c] = x[max(j - u, from) * ld + col[c]];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float v = fabsf(to_f32<T>(y[u][c]));
+        if (s.nan[c] < 0 && v != v) s.nan[c] = max(j - u, from);
+        if (s.inf[c] < 0 && v == INFINITY) s.inf[c] = max(j - u, from);
+      }
+  }
+  return s;
+}
+// Whether a sum x at column c of a row that begins at `start` comes from what the row does not
+// see, or is an infinity that no value is: a NaN (an infinity) among the values it sees
+// explains it.  Every lane of the wave calls it, each with a column of its own.
+__device__ __forceinline__ bool unexplained(float x, const Spoilt& s, int c, int start) {
+  const int n0 = __shfl(s.nan[0], c & 63), n1 = __shfl(s.nan[1], c & 63);
+  const int f0 = __shfl(s.inf[0], c & 63), f1 = __shfl(s.inf[1], c & 63);
+  if (x != x) return (c < 64 ? n0 : n1) < start;
+  return fabsf(x) == INFINITY && (c < 64 ? f0 : f1) < start;
+}
 
 // ------------------------------------------------------------------- forward --
 // The weights exp2(s c - m c) take m c as rounded: a factor that all of a row's weights share,
@@ -578,10 +615,29 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_fwd(AttnArgs<T> a) {
   }
   // a NaN of the sum is one of a weight, and in every column
   const bool lost = sum != sum || far(m, c);
-  if (any_bad<true>(o, in) || __any(in && lost)) {
-    for (int r = 0; r < 32; ++r)
-      if (__builtin_amdgcn_readlane(int(in), r))
-        fwd_row(a, h, kv, w0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(lost), r));
+  bool bad = false;
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) bad = bad || !(fabsf(o[d][v]) < INFINITY);
+  if (__any(in && (bad || lost))) {
+    bool again = lost;
+    if (__any(in && bad && !lost)) {
+      const Spoilt sp = last_spoilt(Vb, a.ldv, min(__builtin_amdgcn_readfirstlane(seq.start), w0), w0, a.D);
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int at = 32 * d + mfma32_row(v, hi);
+          const bool odd = unexplained(o[d][v], sp, at, seq.start);
+          again = again || (at < a.D && odd);
+        }
+    }
+    const uint64_t both = __ballot(in && again);
+    for (uint32_t rows = uint32_t(both) | uint32_t(both >> 32); rows != 0; rows &= rows - 1) {
+      const int r = __ffs(rows) - 1;
+      fwd_row(a, h, kv, w0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(lost), r));
+    }
   }
 }
 
@@ -596,6 +652,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ int32_t cu_lds[kCuLds];
   __shared__ float ms[WAVES][2][32];  // of each wave: reference and sum
+  __shared__ uint32_t again[WAVES];   // rows to form again, for the sake of the wave's columns
   constexpr int TILE = BN * L::kRowBytes;
   char *const kt = smem, *const vt = smem + TILE;
 
@@ -690,23 +747,39 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_fwd_few(AttnArgs<T> a) {
   const int c0 = (2 * w + hi) * PER;
   T* row = a.out + int64_t(min(i, a.N - 1)) * a.ldo + int64_t(h) * a.D;
   bool bad = false;
+  float y[PER];
 #pragma unroll
   for (int e = 0; e < PER; e += 4) {
-    float y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = e; k < e + 4; ++k) {
       y[k] = 0.f;
 #pragma unroll
-      for (int x = 0; x < WAVES; ++x) y[k] += f[x] * part[(x * DP + c0 + e + k) * 32 + col];
-      bad = bad || (c0 + e + k < a.D && !(fabsf(y[k]) < INFINITY));
+      for (int x = 0; x < WAVES; ++x) y[k] += f[x] * part[(x * DP + c0 + k) * 32 + col];
+      bad = bad || (c0 + k < a.D && !(fabsf(y[k]) < INFINITY));
     }
-    if (seq.inside) put4<T, ALIGNED>(row, c0 + e, a.D, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (seq.inside)
+      put4<T, ALIGNED>(row, c0 + e, a.D, y[e] * inv, y[e + 1] * inv, y[e + 2] * inv, y[e + 3] * inv);
   }
   if (seq.inside && hi == 0 && w == 0) a.lse[int64_t(h) * a.N + i] = fmaf(m, c, __builtin_amdgcn_logf(sum)) * kLn2;
   const bool lost = sum != sum || far(m, c);
   if (__syncthreads_or(seq.inside && (bad || lost))) {
+    bool odd = lost;
+    if (__any(seq.inside && bad && !lost)) {
+      const Spoilt sp = last_spoilt(Vb, a.ldv, kmin, i0, a.D);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const bool x = unexplained(y[k], sp, c0 + k, seq.start);
+        odd = odd || (c0 + k < a.D && x);
+      }
+    }
+    const uint64_t both = __ballot(seq.inside && odd);
+    if (lane == 0) again[w] = uint32_t(both) | uint32_t(both >> 32);
+    __syncthreads();
+    uint32_t rows = 0;
+#pragma unroll
+    for (int x = 0; x < WAVES; ++x) rows |= again[x];
     for (int r = w; r < 32; r += WAVES)
-      if (__builtin_amdgcn_readlane(int(seq.inside), r))
+      if ((rows >> r) & 1)
         fwd_row(a, h, kv, i0 + r, __builtin_amdgcn_readlane(seq.start, r), __builtin_amdgcn_readlane(int(lost), r));
   }
 }
@@ -845,7 +918,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
 #pragma unroll
     for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, g[d], a.scale);
   }
-  if (any_bad<false>(g, in)) {
+  if (any_nan<NB>(g, in)) {
     for (int r = 0; r < 32; ++r)
       if (__builtin_amdgcn_readlane(int(in), r)) dq_row(a, h, kv, w0 + r, __builtin_amdgcn_readlane(seq.start, r));
   }
@@ -1032,7 +1105,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dkv(AttnArgs<T> a) {
 #pragma unroll
       for (int d = 0; d < NB; ++d) put_block<T, ALIGNED>(row, d, a.D, g[d], f);
     }
-    if (!any_bad<false>(g, in)) continue;
+    if (!any_nan<NB>(g, in)) continue;
     for (int x = 0; x < 32; ++x) {
       if (!__builtin_amdgcn_readlane(int(in), x)) continue;
       const int end = __builtin_amdgcn_readlane(seq.end, x);

@@ -76,3 +76,31 @@ def test_values_near_the_largest(D, lens, Hq, Hkv, dt):
     rel = (2 * (D + 4) * worst + n + 16) * F32 + (2 * 2.0 ** -8 if dt == "bf16" else F32)
     assert torch.isfinite(O).all() and torch.all((O.double() - want).abs() <= rel * want)
     assert torch.all((lse.double() - wlse).abs() <= ((D + 4) * worst + 4 * wlse.abs() + n + 8) * F32)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lens, Hq, Hkv", FORMS)
+@pytest.mark.parametrize("D", [40, 64, 77, 128])
+def test_infinities_and_nan_that_rows_see_or_not(D, lens, Hq, Hkv, dt):
+    # in the last sequence: column 3 is infinite from a key on, and again, with the other sign, behind a
+    # later one; column 5 is NaN from a third on; the last key, that its own row alone sees, is
+    # spoilt in every column of another kind.  The other columns and rows are as without
+    g = torch.Generator(device=DEV).manual_seed(D)
+    N, n = sum(lens), lens[-1]
+    first = N - n
+    q, k, v = (torch.randn(N, h, D, generator=g, device=DEV).to(DT[dt]) for h in (Hq, Hkv, Hkv))
+    clean, clse = lac.stage_attn(q, k, v, edges(lens))
+    a, b, c = first + 9, first + n // 2, first + n // 2 + 40
+    v[a, :, 3], v[b, :, 3], v[c, :, 5] = float("inf"), -float("inf"), float("nan")
+    v[N - 1, :, ::2], v[N - 1, :, 1::2] = float("nan"), float("inf")
+    O, lse = lac.stage_attn(q, k, v, edges(lens))
+    assert torch.equal(lse, clse)
+    row = torch.arange(N, device=DEV)
+    spoilt = torch.zeros(O.shape, dtype=torch.bool, device=DEV)
+    assert torch.all(O[(row >= a) & (row < b), :, 3] == float("inf")) and torch.isnan(O[b:, :, 3]).all()
+    assert torch.isnan(O[c:, :, 5]).all() and not torch.isfinite(O[N - 1]).any()
+    spoilt[a:, :, 3], spoilt[c:, :, 5], spoilt[N - 1] = True, True, True
+    # a row formed again adds up in another order, and its weights are not rounded to bf16
+    tol = 2.0 ** -6 if dt == "bf16" else 1e-5
+    off = (O.float() - clean.float()).abs()
+    assert torch.isfinite(O[~spoilt]).all() and torch.all(off[~spoilt] <= tol * (1 + clean[~spoilt].float().abs()))
