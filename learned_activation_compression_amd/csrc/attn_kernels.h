@@ -173,6 +173,7 @@ struct Stager {
   using L = Tile<T, DP>;
   static constexpr int PER = ROWS * L::kSlots / 64 / WAVES;
   static_assert(PER > 0 && ROWS * L::kSlots % (64 * WAVES) == 0, "whole copies");
+  static_assert(uint64_t(ROWS) * (sizeof(float) << 22) <= 1ull << 31, "a tile's offsets, rows of 2^22 elements, have 32 bits");
   uint32_t ld;  // bytes of a row
   int D;
   uint32_t off[PER];
@@ -346,8 +347,8 @@ __device__ __forceinline__ bool any_nan(const f32x16 (&x)[NB], bool in) {
 
 // One row at a time, by a wave: 64 rows of the other side in its lanes for their products
 // with it, then the columns l and l + 64 of the sum in its lanes.  Some 250 times as slow as
-// the matrix products, for the few rows beside a masked NaN; a sum that is NaN throughout, as
-// in a step whose gradients are, ends the row at once.
+// the matrix products, for the few rows beside a masked NaN or at the ends of fp32; a sum
+// that is NaN throughout, as in a step whose gradients are, ends the row at once.
 template <typename T>
 __device__ __forceinline__ float dot_row(const T* x, const T* y, int D) {
   float s = 0.f;
@@ -448,10 +449,11 @@ __device__ __forceinline__ void fwd_row(const AttnArgs<T>& a, int h, int kv, int
 // o = sum exp(s - m) v / l with l = sum exp(s - m), in one pass over the keys: a running
 // reference m per row, the sums scaled where it moves.  Two products a pair of rows, 4 D
 // operations, and 5 vector operations a score (factor and difference, exp, sum, maximum,
-// half a rounding), which at 64 columns take twice the products' cycles: the kernel is
-// bound by the issue of both (vector units busy 60 %, matrix units 30 %, some instruction
-// issued in 92 % of the cycles).  32 query rows a wave and two waves a SIMD: one wave's
-// softmax runs beside the other's products.  64 rows a wave, 8 waves a block, tiles of 128
+// half a rounding).  32 query rows a wave and two waves a SIMD: one wave's softmax runs
+// beside the other's products.  No unit is full: at 64 columns a vector instruction is
+// being issued in 60 % of a SIMD's cycles and its matrix unit is busy in 30 % (at 128: 52 and
+// 55), while a wave waits for a barrier or for LDS through 33 % (19) of its cycles and, ready,
+// for its turn through 29 (35).  64 rows a wave, 8 waves a block, tiles of 128
 // keys, and a loop without the turn's overlap were measured and none is faster.
 // bf16: 16384 rows of 16 x 64 in sequences of 2048 101 us (681 TFLOP/s of unmasked pairs),
 // 16384 rows of 16 x 128 in one sequence 1.03-1.09 ms (1.01-1.07 PFLOP/s; the library's product
@@ -807,7 +809,9 @@ __device__ __forceinline__ void dq_row(const AttnArgs<T>& a, int h, int kv, int 
 // partial matrix a block.  For k_attn_dkv the kernel leaves -lse / scale and -delta of every row.
 // bf16: 16384 rows of 16 x 64 in sequences of 1 to 4099 171 us (753 TFLOP/s); 8192 of 16 x 128 in
 // sequences of 2048 130 us (793).
-// Bound by issue as the forward pass, with 4 vector operations a score.
+// The matrix unit is busy in 38 % of the cycles, and vector instructions are issued in 53 % (128
+// columns: 31), 4 a score: a tile's scores, weights, roundings and second products are one
+// chain, with the other wave of the SIMD alone beside it.
 template <typename T, int DP, int WAVES, int BN, int OCC, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES, OCC) void k_attn_dq(AttnArgs<T> a) {
   using L = Tile<T, DP>;
@@ -949,7 +953,9 @@ __device__ __forceinline__ void dkv_row(const AttnArgs<T>& a, int kv, int j, int
 // gV = sum_i p gO and gK = scale sum_i p (gO . v - delta) q: four products a pair of rows, a
 // wave's rows being key rows; the query heads of a group one after the other, into the
 // same sums, so that shared heads need no further pass.
-// Bound by issue and, at 128 columns, by registers.  bf16: 16384 rows of 16 x 64 in 4 key heads,
+// One chain a tile as for gQ (matrix unit busy in 37 to 38 % of the cycles, vector instructions
+// issued in 35 %, at 128 columns 28) and, at 128 columns, few registers.  fp32 has one wave a
+// SIMD and no other beside its chain (matrix unit 37 %).  bf16: 16384 rows of 16 x 64 in 4 key heads,
 // sequences of 1 to 4099, 220-235 us and 16 to join (730-780 TFLOP/s); 8192 of 16 x 128, sequences
 // of 2048, 156-174 us (790-880).  K in LDS and 8 waves a block (313 us for 257), operands read
 // ahead of their products (243 for 252 at 64 columns, registers spilled at 128) and masks

@@ -17,7 +17,7 @@ int check_attn_shape(int64_t N, int64_t Hq, int64_t Hkv, int64_t D) {
 // rows of `heads` heads: leading dimensions
 bool short_rows(int64_t heads, int64_t D, std::initializer_list<int64_t> lds) {
   for (int64_t ld : lds)
-    if (ld < heads * D || ld > (int64_t(1) << 22)) return true;  // a tile's rows lie within 2^30 bytes
+    if (ld < heads * D || ld > (int64_t(1) << 22)) return true;  // a tile's 128 rows at most: 2^31 bytes
   return false;
 }
 

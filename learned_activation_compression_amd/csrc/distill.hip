@@ -352,7 +352,8 @@ __global__ __launch_bounds__(THREADS) void k_distill_bwd(DistillArgs<T> a) {
 // ------------------------------------------------------------------- launches --
 // Rows that fill the card have a block of 256 threads each.  Fewer have one of 1024, and
 // where those leave half of the CUs without work and a row is long, a row is split into
-// slices of 32768 logits at least (one block reads so many in the time of a launch).
+// slices of 32768 logits at least, where the launch that joins them is paid for (4 rows of fp32:
+// 65536 logits 11.5 us in two, 12.3 whole; 131072 11.6 in four, 17.7 whole; slices of 16384 the same).
 constexpr int64_t kManyRows = 1024, kSlice = 32768;
 int split(int64_t N, int64_t V) {
   const int64_t want = (128 + N - 1) / N, most = V / kSlice;

@@ -9,8 +9,9 @@
 //    operand load of a wave is one contiguous kilobyte, from memory or LDS.
 //  - exponents, one byte each, [KB][rows rounded up to 256], then 256 bytes of
 //    slack, so that 256 bytes from the first row of any tile can be read.
-// Codes of padding rows are zero or stale: they only reach output rows that are
-// not stored.  Padding columns are zero in every pack.
+// Codes and exponents of padding rows only reach output rows that are not stored: codes
+// up to the next multiple of 32 rows are zero, exponents behind it whatever was there.
+// Padding columns are zero in every pack.
 #pragma once
 
 #include "common.h"

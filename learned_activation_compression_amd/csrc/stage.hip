@@ -293,7 +293,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_stage_norm(NormArgs<T> a) {
 // 128: its largest magnitude is found among 16 neighbouring lanes, and its codes are half of
 // a row's 16-byte piece.  e4m3 has few values, and an element near the middle of two goes to
 // one or the other by the last bits of the sums; so the row's roots and the products with
-// them are fp64 (16384 x 1024 bf16 in 28.5 us, 4.1 TB/s; 24.3 in fp32 throughout).
+// them are fp64, and so is what the codes and bf16 numbers are rounded from (16384 x 1024
+// bf16 in 30 us, 3.9 TB/s; 28.5 with outputs by way of fp32, 24.3 in fp32 throughout).
 __device__ __forceinline__ double squares8(const float* v) {  // by pairs: three roundings deep
   float q[8];
 #pragma unroll
